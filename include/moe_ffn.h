@@ -296,6 +296,97 @@ MOE_API moe_status moe_ffn_down_batched(const moe_ffn_desc* d, const uint16_t* a
                                         const int32_t* counts, int32_t capacity, float* yb,
                                         hipStream_t stream);
 
+/* Element types of the products on ragged rows and of the MXFP4 calls below. */
+typedef enum {
+  MOE_DTYPE_F32 = 0,
+  MOE_DTYPE_BF16 = 1,
+  MOE_DTYPE_F16 = 2,
+  MOE_DTYPE_MXFP4 = 3   /* OCP microscaled E2M1: codes uint8 [..][K/2], element 2i in the low and
+                           2i+1 in the high nibble of byte i; exponents uint8 E8M0 [..][K/32];
+                           value = e2m1(code) * 2^(exponent - 127), NaN where the exponent is 255 */
+} moe_dtype;
+
+/* A product on rows grouped by expert with ragged counts: P2's grouped GEMM
+ * Y_e = X_e W_e^T ("Hardware-Native Joint Sparse-Quantization for Trillion-
+ * Scale MoE", Section 2) without padding or capacity. Expert e owns rows
+ * offsets[e] .. offsets[e + 1] - 1 of the row operands; `offsets` is int32
+ * [E + 1] on the device, non-decreasing, so no host synchronisation sizes
+ * anything (App. D.1). Rows before offsets[0] and from offsets[E] on belong to
+ * no expert: they are neither read nor written. Whatever the array holds, it is
+ * taken as clamped to [0, rows] and raised to the largest entry before it.
+ * Row operands are [rows][cols] with a stride of ld elements between rows (>=
+ * cols, a multiple of 8, at most 2^22) and 16-byte aligned; w and dw are
+ * contiguous and 16-byte aligned. Outputs may not overlap inputs. */
+typedef struct {
+  int32_t rows;       /* rows of the row operands (>= 0) */
+  int32_t E;          /* experts (1..2048) */
+  int32_t N;          /* output features: rows of an expert's weights; a multiple of 8, at most 2^20 */
+  int32_t K;          /* input features; a multiple of 8 (MXFP4: of 32), at most 2^20 */
+  int32_t dtype;      /* moe_dtype of x, w, dy: MOE_DTYPE_BF16 or _F16 (moe_grouped_matmul_mxfp4: _MXFP4) */
+  int32_t out_dtype;  /* the same, or MOE_DTYPE_F32 (moe_grouped_matmul_mxfp4: _BF16, _F16 or _F32) */
+} moe_grouped_matmul_desc;
+
+/* y[r][n] = sum_k x[r][k] w[e][n][k] for every row r of expert e. fp32 sums,
+ * rounded once to out_dtype. rows == 0 is a no-op.
+ *   x [rows][K] (stride ldx), w [E][N][K], y [rows][N] (stride ldy)
+ * Errors of this and the next three calls: MOE_ERR_INVALID_ARG (null or
+ * misaligned pointers, sizes, types, strides), MOE_ERR_UNSUPPORTED (limits
+ * above, or more than 2^30 tasks), MOE_ERR_HIP. */
+MOE_API moe_status moe_grouped_matmul(const moe_grouped_matmul_desc* d, const void* x, int64_t ldx, const void* w,
+                                      const int32_t* offsets, void* y, int64_t ldy, hipStream_t stream);
+
+/* Gradient of moe_grouped_matmul with respect to x:
+ * dx[r][k] = sum_n dy[r][n] w[e][n][k].
+ *   dy [rows][N] (stride lddy), w [E][N][K], dx [rows][K] (stride lddx) */
+MOE_API moe_status moe_grouped_matmul_dx(const moe_grouped_matmul_desc* d, const void* dy, int64_t lddy,
+                                         const void* w, const int32_t* offsets, void* dx, int64_t lddx,
+                                         hipStream_t stream);
+
+/* Gradient of moe_grouped_matmul with respect to w:
+ * dw[e][n][k] = sum over e's rows of dy[r][n] x[r][k], every element written
+ * (zero for an expert without rows, also when rows == 0).
+ *   dy [rows][N] (stride lddy), x [rows][K] (stride ldx), dw [E][N][K] */
+MOE_API moe_status moe_grouped_matmul_dw(const moe_grouped_matmul_desc* d, const void* dy, int64_t lddy,
+                                         const void* x, int64_t ldx, const int32_t* offsets, void* dw,
+                                         hipStream_t stream);
+
+/* moe_grouped_matmul on MXFP4 operands (both x and w), by the matrix
+ * instructions' own block scaling: exact products, fp32 sums.
+ *   xq [rows][K/2], x_scale [rows][K/32], wq [E][N][K/2], w_scale [E][N][K/32]
+ *   (contiguous; xq and wq 16-byte aligned), y [rows][N] (stride ldy) */
+MOE_API moe_status moe_grouped_matmul_mxfp4(const moe_grouped_matmul_desc* d, const void* xq,
+                                            const uint8_t* x_scale, const void* wq, const uint8_t* w_scale,
+                                            const int32_t* offsets, void* y, int64_t ldy, hipStream_t stream);
+
+/* Rows of K elements (K a multiple of 32, at most 2^20) to MXFP4. For a block
+ * of 32 with largest magnitude m the exponent is
+ * clamp(floor(log2 m) - 2, -127, 127) (-127 for m == 0); an element x becomes
+ * the E2M1 value nearest to x / 2^exponent, ties to the even code, saturating
+ * at +-6. A block that holds an infinity or a NaN gets exponent byte 255 and
+ * codes 0, so that it decodes to NaN.
+ *   dtype  MOE_DTYPE_BF16, _F16 or _F32: the type of x [rows][K] (stride ldx
+ *          elements, a multiple of 8; 16-byte aligned)
+ *   q      uint8 [rows][K/2] out, 16-byte aligned; scale uint8 [rows][K/32] out
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (limits), MOE_ERR_HIP. */
+MOE_API moe_status moe_mxfp4_quantize(int32_t dtype, const void* x, int64_t ldx, int64_t rows, int32_t K, void* q,
+                                      uint8_t* scale, hipStream_t stream);
+
+/* The values MXFP4 rows stand for, exact: y [rows][K] (stride ldy) of type
+ * MOE_DTYPE_BF16 or _F32 (fp16 has not the range: MOE_ERR_UNSUPPORTED). Values
+ * past fp32's range become infinite. Arguments and errors as moe_mxfp4_quantize. */
+MOE_API moe_status moe_mxfp4_dequantize(int32_t dtype, const void* q, const uint8_t* scale, int64_t rows, int32_t K,
+                                        void* y, int64_t ldy, hipStream_t stream);
+
+/* Row offsets of an alignment, as the calls above take them:
+ * offsets[e] = b * (blocks of experts below e), int32 [E + 1], from
+ * moe_align's expert_block_ids (`blocks` entries: capacity / b), num_padded
+ * and b. With b == 1 the aligned rows have no padding, and expert e's are
+ * sorted_route_ids[offsets[e]] .. [offsets[e + 1] - 1].
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (E > 2048, blocks * b above
+ * INT32_MAX), MOE_ERR_HIP. */
+MOE_API moe_status moe_align_offsets(const int32_t* expert_block_ids, const int32_t* num_padded, size_t blocks,
+                                     int32_t E, int32_t b, int32_t* offsets, hipStream_t stream);
+
 /* Number of kernels moe_ffn_forward launches for this description (0 on error). */
 MOE_API int32_t moe_ffn_kernel_count(const moe_ffn_desc* d);
 

@@ -30,7 +30,13 @@ MOE_PATH_AUTO = 0
 MOE_PATH_DECODE = 1
 MOE_PATH_GROUPED = 2
 
+MOE_DTYPE_F32 = 0
+MOE_DTYPE_BF16 = 1
+MOE_DTYPE_F16 = 2
+MOE_DTYPE_MXFP4 = 3
+
 _c_i32 = ctypes.c_int32
+_c_i64 = ctypes.c_int64
 _c_size = ctypes.c_size_t
 _c_ptr = ctypes.c_void_p
 
@@ -44,6 +50,11 @@ class moe_ffn_desc(ctypes.Structure):
     _fields_ = [("M", _c_i32), ("H", _c_i32), ("I", _c_i32), ("E", _c_i32), ("k", _c_i32),
                 ("b", _c_i32), ("w13", moe_weights), ("w2", moe_weights), ("path", _c_i32),
                 ("max_workgroups", _c_i32), ("expert_base", _c_i32)]
+
+
+class moe_grouped_matmul_desc(ctypes.Structure):
+    _fields_ = [("rows", _c_i32), ("E", _c_i32), ("N", _c_i32), ("K", _c_i32), ("dtype", _c_i32),
+                ("out_dtype", _c_i32)]
 
 
 class MoeError(RuntimeError):
@@ -81,6 +92,17 @@ _SIGNATURES = {
                                          _c_ptr, _c_ptr]),
     "moe_ffn_down_batched": (_c_i32, [ctypes.POINTER(moe_ffn_desc), _c_ptr, _c_ptr, _c_ptr, _c_i32,
                                       _c_ptr, _c_ptr]),
+    "moe_grouped_matmul": (_c_i32, [ctypes.POINTER(moe_grouped_matmul_desc), _c_ptr, _c_i64, _c_ptr, _c_ptr,
+                                    _c_ptr, _c_i64, _c_ptr]),
+    "moe_grouped_matmul_dx": (_c_i32, [ctypes.POINTER(moe_grouped_matmul_desc), _c_ptr, _c_i64, _c_ptr, _c_ptr,
+                                       _c_ptr, _c_i64, _c_ptr]),
+    "moe_grouped_matmul_dw": (_c_i32, [ctypes.POINTER(moe_grouped_matmul_desc), _c_ptr, _c_i64, _c_ptr, _c_i64,
+                                       _c_ptr, _c_ptr, _c_ptr]),
+    "moe_grouped_matmul_mxfp4": (_c_i32, [ctypes.POINTER(moe_grouped_matmul_desc), _c_ptr, _c_ptr, _c_ptr, _c_ptr,
+                                          _c_ptr, _c_ptr, _c_i64, _c_ptr]),
+    "moe_mxfp4_quantize": (_c_i32, [_c_i32, _c_ptr, _c_i64, _c_i64, _c_i32, _c_ptr, _c_ptr, _c_ptr]),
+    "moe_mxfp4_dequantize": (_c_i32, [_c_i32, _c_ptr, _c_ptr, _c_i64, _c_i32, _c_ptr, _c_i64, _c_ptr]),
+    "moe_align_offsets": (_c_i32, [_c_ptr, _c_ptr, _c_size, _c_i32, _c_i32, _c_ptr, _c_ptr]),
     "moe_ffn_kernel_count": (_c_i32, [ctypes.POINTER(moe_ffn_desc)]),
     "moe_ffn_kernel_name": (ctypes.c_char_p, [ctypes.POINTER(moe_ffn_desc), _c_i32]),
     "moe_ffn_intermediate": (_c_i32, [ctypes.POINTER(moe_ffn_desc), ctypes.POINTER(_c_size),
@@ -407,3 +429,221 @@ def moe_ffn_auto_decode_max_m() -> int:
 def moe_ffn_resolved_path(desc: moe_ffn_desc) -> int:
     """The path moe_ffn_forward takes for `desc` (-1 if it is rejected)."""
     return int(lib().moe_ffn_resolved_path(ctypes.byref(desc)))
+
+
+# ---------------------------------------------------------------------------
+# Products on rows grouped by expert with ragged counts, MXFP4, row offsets
+# ---------------------------------------------------------------------------
+
+_dtype_codes = {}
+
+
+def _dtype_code(name, t, allowed) -> int:
+    """moe_dtype of tensor ``t``; TypeError unless it is one of ``allowed``."""
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16,
+                             torch.float16: MOE_DTYPE_F16})
+    code = _dtype_codes.get(getattr(t, "dtype", None))
+    if code not in allowed:
+        if not hasattr(t, "data_ptr"):
+            raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+        raise TypeError(f"{name}: unexpected dtype {t.dtype}")
+    return code
+
+
+def _expect_rows(name, t, shape, device=None):
+    """Check a row operand: a 2-d tensor of ``shape`` on a GPU (on ``device``
+    when given) whose rows are contiguous. Returns its row stride in elements
+    (the library checks the stride's own rules)."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    rows, cols = shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous, got strides {t.stride()}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must be on a GPU, got {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    return t.stride(0) if rows > 1 else -(-cols // 8) * 8
+
+
+def _call_on(device, stream, fn, *args) -> int:
+    """fn(*args, stream) with ``device`` current; ``stream`` None is the
+    device's current stream."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    raw = getattr(stream, "cuda_stream", stream)
+    if device.index == torch.cuda.current_device():
+        return fn(*args, raw)
+    with torch.cuda.device(device):
+        return fn(*args, raw)
+
+
+_GMM_TYPES = (MOE_DTYPE_BF16, MOE_DTYPE_F16)
+_ALL_TYPES = (MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16)
+
+
+def _expect_3d(name, t):
+    if not hasattr(t, "data_ptr"):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected [E, N, K], got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def moe_grouped_matmul(x, w, offsets, y, stream=None, check: bool = True) -> int:
+    """y[r] = w[e] x[r] for the rows r of every expert e.
+
+    x [rows, K] and w [E, N, K] bf16 or fp16, offsets [E + 1] int32 (expert e owns
+    rows offsets[e] .. offsets[e + 1] - 1), y [rows, N] of x's dtype or fp32. x and
+    y may have a row stride. Rows no expert owns are left as they were."""
+    import torch
+    E, N, K = _expect_3d("w", w)
+    dt = _dtype_code("x", x, _GMM_TYPES)
+    out = _dtype_code("y", y, (dt, MOE_DTYPE_F32))
+    rows = x.shape[0] if x.dim() == 2 else -1
+    ldx = _expect_rows("x", x, (rows, K))
+    _expect("w", w, x.dtype, (E, N, K), x.device)
+    _expect("offsets", offsets, torch.int32, (E + 1,), x.device)
+    ldy = _expect_rows("y", y, (rows, N), x.device)
+    d = moe_grouped_matmul_desc(rows, E, N, K, dt, out)
+    st = _call_on(x.device, stream, lib().moe_grouped_matmul, ctypes.byref(d), x.data_ptr(), ldx, w.data_ptr(),
+                  offsets.data_ptr(), y.data_ptr(), ldy)
+    if check:
+        _check(st, "moe_grouped_matmul")
+    return st
+
+
+def moe_grouped_matmul_dx(dy, w, offsets, dx, stream=None, check: bool = True) -> int:
+    """Gradient of moe_grouped_matmul with respect to x: dx[r] = w[e]^T dy[r].
+
+    dy [rows, N] and w [E, N, K] bf16 or fp16, offsets as there, dx [rows, K] of
+    dy's dtype or fp32."""
+    import torch
+    E, N, K = _expect_3d("w", w)
+    dt = _dtype_code("dy", dy, _GMM_TYPES)
+    out = _dtype_code("dx", dx, (dt, MOE_DTYPE_F32))
+    rows = dy.shape[0] if dy.dim() == 2 else -1
+    lddy = _expect_rows("dy", dy, (rows, N))
+    _expect("w", w, dy.dtype, (E, N, K), dy.device)
+    _expect("offsets", offsets, torch.int32, (E + 1,), dy.device)
+    lddx = _expect_rows("dx", dx, (rows, K), dy.device)
+    d = moe_grouped_matmul_desc(rows, E, N, K, dt, out)
+    st = _call_on(dy.device, stream, lib().moe_grouped_matmul_dx, ctypes.byref(d), dy.data_ptr(), lddy, w.data_ptr(),
+                  offsets.data_ptr(), dx.data_ptr(), lddx)
+    if check:
+        _check(st, "moe_grouped_matmul_dx")
+    return st
+
+
+def moe_grouped_matmul_dw(dy, x, offsets, dw, stream=None, check: bool = True) -> int:
+    """Gradient of moe_grouped_matmul with respect to w: dw[e] = sum of
+    dy[r] x[r]^T over e's rows (zero for an expert without rows).
+
+    dy [rows, N] and x [rows, K] bf16 or fp16, offsets as there, dw [E, N, K] of
+    their dtype or fp32."""
+    import torch
+    E, N, K = _expect_3d("dw", dw)
+    dt = _dtype_code("dy", dy, _GMM_TYPES)
+    out = _dtype_code("dw", dw, (dt, MOE_DTYPE_F32))
+    rows = dy.shape[0] if dy.dim() == 2 else -1
+    lddy = _expect_rows("dy", dy, (rows, N))
+    if x.dtype != dy.dtype:
+        raise TypeError(f"x: expected dtype {dy.dtype}, got {x.dtype}")
+    ldx = _expect_rows("x", x, (rows, K), dy.device)
+    _expect("offsets", offsets, torch.int32, (E + 1,), dy.device)
+    _expect("dw", dw, dw.dtype, (E, N, K), dy.device)
+    d = moe_grouped_matmul_desc(rows, E, N, K, dt, out)
+    st = _call_on(dy.device, stream, lib().moe_grouped_matmul_dw, ctypes.byref(d), dy.data_ptr(), lddy, x.data_ptr(),
+                  ldx, offsets.data_ptr(), dw.data_ptr())
+    if check:
+        _check(st, "moe_grouped_matmul_dw")
+    return st
+
+
+def moe_grouped_matmul_mxfp4(xq, x_scale, wq, w_scale, offsets, y, stream=None, check: bool = True) -> int:
+    """moe_grouped_matmul on MXFP4 operands (moe_mxfp4_quantize's layout).
+
+    xq [rows, K/2], x_scale [rows, K/32], wq [E, N, K/2], w_scale [E, N, K/32] uint8,
+    offsets as there, y [rows, N] bf16, fp16 or fp32."""
+    import torch
+    E, N, half = _expect_3d("wq", wq)
+    K = 2 * half
+    out = _dtype_code("y", y, _ALL_TYPES)
+    rows = xq.shape[0]
+    dev = _expect("xq", xq, torch.uint8, (rows, half))
+    _expect("x_scale", x_scale, torch.uint8, (rows, K // 32), dev)
+    _expect("wq", wq, torch.uint8, (E, N, half), dev)
+    _expect("w_scale", w_scale, torch.uint8, (E, N, K // 32), dev)
+    _expect("offsets", offsets, torch.int32, (E + 1,), dev)
+    ldy = _expect_rows("y", y, (rows, N), dev)
+    d = moe_grouped_matmul_desc(rows, E, N, K, MOE_DTYPE_MXFP4, out)
+    st = _call_on(dev, stream, lib().moe_grouped_matmul_mxfp4, ctypes.byref(d), xq.data_ptr(), x_scale.data_ptr(),
+                  wq.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(), y.data_ptr(), ldy)
+    if check:
+        _check(st, "moe_grouped_matmul_mxfp4")
+    return st
+
+
+def _mxfp4_rows(name, t, q, scale):
+    """(rows, K, row stride) of the values ``t`` [.., K] beside codes ``q`` [.., K/2]
+    and exponents ``scale`` [.., K/32]."""
+    import torch
+    if t.dim() < 2:
+        raise ValueError(f"{name}: expected [.., K], got shape {tuple(t.shape)}")
+    lead, K = tuple(t.shape[:-1]), t.shape[-1]
+    if t.dim() == 2:
+        ld = _expect_rows(name, t, (lead[0], K))
+    else:
+        _expect(name, t, t.dtype, t.shape)
+        ld = K
+    _expect("q", q, torch.uint8, lead + (K // 2,), t.device)
+    _expect("scale", scale, torch.uint8, lead + (K // 32,), t.device)
+    rows = 1
+    for n in lead:
+        rows *= n
+    return rows, K, ld
+
+
+def moe_mxfp4_quantize(x, q, scale, stream=None, check: bool = True) -> int:
+    """Values x [.., K] (bf16, fp16 or fp32; K a multiple of 32; a 2-d x may have a
+    row stride) to MXFP4: codes q [.., K/2] and E8M0 exponents scale [.., K/32], uint8."""
+    dt = _dtype_code("x", x, _ALL_TYPES)
+    rows, K, ld = _mxfp4_rows("x", x, q, scale)
+    st = _call_on(x.device, stream, lib().moe_mxfp4_quantize, dt, x.data_ptr(), ld, rows, K, q.data_ptr(),
+                  scale.data_ptr())
+    if check:
+        _check(st, "moe_mxfp4_quantize")
+    return st
+
+
+def moe_mxfp4_dequantize(q, scale, y, stream=None, check: bool = True) -> int:
+    """The values MXFP4 codes q [.., K/2] and exponents scale [.., K/32] stand for,
+    exact: y [.., K] bf16 or fp32 (a 2-d y may have a row stride)."""
+    dt = _dtype_code("y", y, (MOE_DTYPE_F32, MOE_DTYPE_BF16))
+    rows, K, ld = _mxfp4_rows("y", y, q, scale)
+    st = _call_on(y.device, stream, lib().moe_mxfp4_dequantize, dt, q.data_ptr(), scale.data_ptr(), rows, K,
+                  y.data_ptr(), ld)
+    if check:
+        _check(st, "moe_mxfp4_dequantize")
+    return st
+
+
+def moe_align_offsets(expert_block_ids, num_padded, E: int, b: int, offsets, stream=None,
+                      check: bool = True) -> int:
+    """Row offsets [E + 1] int32 of moe_align's blocks, as moe_grouped_matmul takes
+    them; with b == 1 expert e's routes are sorted_route_ids[offsets[e]:offsets[e + 1]]."""
+    import torch
+    if not hasattr(expert_block_ids, "data_ptr"):
+        raise TypeError(f"expert_block_ids: expected a torch.Tensor, got {type(expert_block_ids).__name__}")
+    n = expert_block_ids.numel()
+    dev = _expect("expert_block_ids", expert_block_ids, torch.int32, (n,))
+    _expect("num_padded", num_padded, torch.int32, (1,), dev)
+    _expect("offsets", offsets, torch.int32, (E + 1,), dev)
+    st = _call_on(dev, stream, lib().moe_align_offsets, expert_block_ids.data_ptr(), num_padded.data_ptr(), n, E, b,
+                  offsets.data_ptr())
+    if check:
+        _check(st, "moe_align_offsets")
+    return st

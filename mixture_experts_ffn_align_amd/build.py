@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_ffn.so")
-SOURCES = ["api.hip", "align.hip", "decode.hip", "grouped.hip"]
+SOURCES = ["api.hip", "align.hip", "decode.hip", "grouped.hip", "ragged_api.hip", "ragged.hip", "mxfp4.hip"]
 # Measurement kernels (streaming-read floor, copy peak) for bench.py.
 BENCH_LIB = os.path.join(PKG, "libmoe_bench.so")
 BENCH_SOURCES = ["bench_kernels.hip"]

@@ -291,6 +291,27 @@ __global__ __launch_bounds__(kThreads) void align_scatter(
   place_loaded(ev, r0, r1, E, nbits, off, run, wcnt, sorted);
 }
 
+constexpr int kOffsetThreads = 256;
+
+// offsets[e] = b * (number of blocks of experts below e): blocks are in expert
+// order, so a binary search finds each boundary; no pass over the blocks.
+__global__ __launch_bounds__(kOffsetThreads) void align_offsets(const int32_t* __restrict__ blocks,
+                                                          const int32_t* __restrict__ num_padded, int nblk, int E,
+                                                          int b, int32_t* __restrict__ offsets) {
+  const int e = blockIdx.x * kOffsetThreads + threadIdx.x;
+  if (e > E) return;
+  const int live = min(nblk, max(0, num_padded[0]) / b);
+  int lo = 0, hi = live;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo) / 2;
+    if (blocks[mid] < e)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  offsets[e] = lo * b;
+}
+
 }  // namespace
 
 size_t align_lds_bytes(int E) {
@@ -325,6 +346,13 @@ hipError_t launch_align(const int32_t* ids, int mk, int E, int ebase, int b, int
   launch(align_colscan, dim3((E + 255) / 256), dim3(256), 0, stream, counts, G, E, totals);
   launch(align_scatter, dim3(G), dim3(kThreads), lds, stream, ids, mk, E, ebase, b, nbits,
                      kAlignRoutesPerGroup, counts, totals, sorted, blocks, num_padded, cap);
+  return hipGetLastError();
+}
+
+hipError_t launch_align_offsets(const int32_t* blocks, const int32_t* num_padded, int nblk, int E, int b,
+                                int32_t* offsets, hipStream_t stream) {
+  launch(align_offsets, dim3((E + kOffsetThreads) / kOffsetThreads), dim3(kOffsetThreads), 0, stream, blocks, num_padded, nblk, E,
+         b, offsets);
   return hipGetLastError();
 }
 

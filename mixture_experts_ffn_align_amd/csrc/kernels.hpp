@@ -105,4 +105,31 @@ hipError_t launch_combine(const GroupedArgs& p, hipStream_t stream);
 hipError_t launch_grouped_gate_up_batched(const GroupedArgs& p, const int32_t* counts, int cap, hipStream_t stream);
 hipError_t launch_grouped_down_batched(const GroupedArgs& p, const int32_t* counts, int cap, hipStream_t stream);
 
+// Products on rows grouped by expert with ragged counts (ragged.hip). `a` is
+// the operand whose index runs along the output's contiguous dimension.
+struct RaggedArgs {
+  const void* a;            // forward, input gradient: w [E][N][K]; weight gradient: x
+  const void* b;            // forward: x; input and weight gradient: dy
+  const uint8_t* a_scale;   // MXFP4 forward: exponents of w [E][N][K/32] and x [rows][K/32]
+  const uint8_t* b_scale;
+  const int32_t* offsets;   // [E + 1]
+  void* out;                // y, dx or dW
+  int64_t lda, ldb, ldo;    // row strides in elements (weights, codes and dW are contiguous)
+  int rows, E, N, K;
+  int out_dtype;            // moe_dtype
+};
+hipError_t launch_ragged_forward(const RaggedArgs& p, int dtype, hipStream_t stream);
+hipError_t launch_ragged_input_grad(const RaggedArgs& p, int dtype, hipStream_t stream);
+hipError_t launch_ragged_weight_grad(const RaggedArgs& p, int dtype, hipStream_t stream);
+
+// MXFP4 (mxfp4.hip). K a multiple of 32; ldx, ldy in elements.
+hipError_t launch_mxfp4_quantize(int dtype, const void* x, int64_t ldx, int64_t rows, int K, void* q, uint8_t* scale,
+                                 hipStream_t stream);
+hipError_t launch_mxfp4_dequantize(int dtype, const void* q, const uint8_t* scale, int64_t rows, int K, void* y,
+                                   int64_t ldy, hipStream_t stream);
+
+// Row offsets of an alignment (align.hip).
+hipError_t launch_align_offsets(const int32_t* blocks, const int32_t* num_padded, int nblk, int E, int b,
+                                int32_t* offsets, hipStream_t stream);
+
 }  // namespace moe

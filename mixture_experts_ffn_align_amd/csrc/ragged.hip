@@ -41,12 +41,16 @@ typedef int intx8 __attribute__((ext_vector_type(8)));
 // Operand element types of the kernel template.
 struct Bf16 {};
 struct F16 {};
-struct Fp4 {};
+struct Fp4 {};      // K a multiple of 128, exponents aligned to 4 bytes: a slab's are aligned words
+struct Fp4Odd {};   // any other K or alignment
 
 enum Kind { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 
-constexpr int kSlabBytes = 128;   // bytes of a direct row per slab
-constexpr int kSlabRows = 64;     // rows of a transposed operand per slab (16-bit elements)
+constexpr int kSteps = 2;                      // matrix steps (32 16-bit elements or 128 codes) per slab
+constexpr int kSlabBytes = 64 * kSteps;        // bytes of a direct row per slab
+constexpr int kSlabRows = 32 * kSteps;         // rows of a transposed operand per slab (16-bit elements)
+constexpr int kCus = 256;
+constexpr int kLdsPerCu = 160 * 1024;
 constexpr int kGroupM = 4;        // row tiles visited together, see find_task
 
 __device__ __align__(16) const uint32_t zero_page[4] = {0, 0, 0, 0};
@@ -61,7 +65,25 @@ __device__ __forceinline__ void dma16_off(const void* base, uint32_t voff, uint3
                : "v"(voff), "s"(base), "s"(lds_base)
                : "memory", "m0");
 }
+
+// The same for the lanes in `lanes` only (all 64 are active before and after).
+// With none it still counts as one load, so waits by count stay right.
+__device__ __forceinline__ void dma16_off_lanes(const void* base, uint32_t voff, uint64_t lanes, uint32_t lds_base) {
+  asm volatile(
+      "s_mov_b32 m0, %2\n\ts_mov_b64 exec, %3\n\tglobal_load_lds_dwordx4 %0, %1\n\ts_mov_b64 exec, -1"
+      :
+      : "v"(voff), "s"(base), "s"(lds_base), "s"(lanes)
+      : "memory", "m0");
+}
 #pragma clang diagnostic pop
+
+// A wave-uniform address made explicitly scalar.
+__device__ __forceinline__ const char* uniform_ptr(const void* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const char*>(uint64_t(hi) << 32 | lo);
+}
 
 template <typename T>
 __device__ __forceinline__ floatx4 mfma_step(const uint4& a, const uint4& b, const floatx4& c) {
@@ -73,31 +95,39 @@ __device__ __forceinline__ floatx4 mfma_step(const uint4& a, const uint4& b, con
                                                    0, 0);
 }
 
-// 128 MXFP4 products per output: a lane's 32 codes are one block, scaled by
-// byte kByte of its scale word.
-template <int kByte>
-__device__ __forceinline__ floatx4 mfma_step_fp4(const uint4& a, const uint4& b, const floatx4& c, int sa, int sb) {
+// 128 MXFP4 products per output: a lane's 32 codes are one block, whose
+// exponent is byte ka (kb) of its word of exponents. Constants after inlining.
+__device__ __forceinline__ floatx4 mfma_step_fp4(const uint4& a, const uint4& b, const floatx4& c, int sa, int ka, int sb,
+                                                 int kb) {
   const intx8 av = {int(a.x), int(a.y), int(a.z), int(a.w), 0, 0, 0, 0};
   const intx8 bv = {int(b.x), int(b.y), int(b.z), int(b.w), 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, kByte, sa, kByte, sb);
+#define MOE_FP4_CASE(A, B) \
+  case 4 * A + B:          \
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, A, sa, B, sb);
+  switch (4 * ka + kb) {
+    MOE_FP4_CASE(0, 0) MOE_FP4_CASE(0, 2) MOE_FP4_CASE(2, 0) MOE_FP4_CASE(2, 2)
+    MOE_FP4_CASE(1, 1) MOE_FP4_CASE(1, 3) MOE_FP4_CASE(3, 1) MOE_FP4_CASE(3, 3)
+  }
+#undef MOE_FP4_CASE
+  return c;
 }
 
-// Start of expert e's rows: offsets clamped to [0, rows] and made
-// non-decreasing, so that whatever the array holds, no row has two owners and
-// no access leaves the operands.
+__device__ __forceinline__ int clamp_row(int v, int lo, int rows) { return min(rows, max(lo, v)); }
+
+// Row tiles of the experts, by lane: lane l holds ceil(E / 64) consecutive ones.
 struct Ranges {
   int first;   // first expert of this lane
-  int start;   // start row of that expert
   int base;    // row tiles before this lane's experts
   int tiles;   // row tiles of this lane's experts
   int total;   // row tiles of all experts
 };
 
-__device__ __forceinline__ int clamp_row(int v, int lo, int rows) { return min(rows, max(lo, v)); }
-
-// Each lane of a wave takes ceil(E / 64) consecutive experts.
+// Reads the offsets once: the start row of every expert goes to starts [E + 1]
+// in LDS, clamped to [0, rows] and made non-decreasing, so that whatever the
+// array holds, no row has two owners and no access leaves the operands. Every
+// wave scans (and stores the same values); the caller puts a barrier behind.
 template <int TB>
-__device__ __forceinline__ Ranges scan_ranges(const int32_t* offsets, int E, int rows, int lane) {
+__device__ __forceinline__ Ranges scan_ranges(const int32_t* offsets, int E, int rows, int* starts, int lane) {
   const int per = (E + 63) / 64;
   Ranges r;
   r.first = min(E, lane * per);
@@ -110,11 +140,12 @@ __device__ __forceinline__ Ranges scan_ranges(const int32_t* offsets, int E, int
     if (lane >= d) top = max(top, o);
   }
   const int before = __shfl_up(top, 1, kWave);
-  const int floor0 = lane == 0 ? 0 : before;
-  r.start = r.first < E ? clamp_row(offsets[r.first], floor0, rows) : rows;
-  int cur = r.start, tiles = 0;
+  int cur = r.first < E ? clamp_row(offsets[r.first], lane == 0 ? 0 : before, rows) : rows;
+  int tiles = 0;
   for (int e = r.first; e < last; ++e) {
     const int nxt = clamp_row(offsets[e + 1], cur, rows);
+    starts[e] = cur;
+    if (e + 1 == E) starts[E] = nxt;
     tiles += (nxt - cur + TB - 1) / TB;
     cur = nxt;
   }
@@ -142,26 +173,20 @@ struct Task {
 // consecutive and go through kGroupM row tiles per column tile, so that the
 // tasks running at one time on one XCD share weights and rows in its L2.
 template <int TB>
-__device__ __forceinline__ Task find_task(const Ranges& r, const int32_t* offsets, int E, int rows, int lane, int L,
-                                          int NT, int TA) {
+__device__ __forceinline__ Task find_task(const Ranges& r, const int* starts, int E, int L, int NT, int TA) {
   const int t = L / NT;
   const uint64_t own = __ballot(t >= r.base && t < r.base + r.tiles);
   const int src = __ffsll(static_cast<unsigned long long>(own)) - 1;
-  int e = r.first, cur = r.start, base = r.base, nxt = cur;
-  if (lane == src) {
-    for (;; ++e) {
-      nxt = clamp_row(offsets[e + 1], cur, rows);
-      const int n = (nxt - cur + TB - 1) / TB;
-      if (t < base + n || e + 1 >= E) break;
-      base += n;
-      cur = nxt;
-    }
+  int e = __builtin_amdgcn_readlane(r.first, src);
+  int base = __builtin_amdgcn_readlane(r.base, src);
+  int cur = uniform(starts[e]), nxt, mt;
+  for (;; ++e) {
+    nxt = uniform(starts[e + 1]);
+    mt = (nxt - cur + TB - 1) / TB;
+    if (t < base + mt || e + 1 >= E) break;
+    base += mt;
+    cur = nxt;
   }
-  e = __builtin_amdgcn_readlane(e, src);
-  cur = __builtin_amdgcn_readlane(cur, src);
-  nxt = __builtin_amdgcn_readlane(nxt, src);
-  base = __builtin_amdgcn_readlane(base, src);
-  const int mt = (nxt - cur + TB - 1) / TB;
   const int local = L - base * NT;
   const int grp = local / (kGroupM * NT);
   const int gm = min(kGroupM, mt - grp * kGroupM);
@@ -197,29 +222,33 @@ __device__ __forceinline__ int trans_unit(int row, int u) {
 
 // One operand's side of the data movement: which bytes this wave brings in.
 // kTrans: the tile is [64 rows][T] (the rows are the summed index).
-template <int T, int NW, bool kTrans>
+// kSkip (direct): rows past the limit are left out, so their LDS holds whatever
+// was there (it only reaches outputs that are not stored).
+template <int T, int NW, bool kTrans, bool kSkip>
 struct Loader {
-  static constexpr int kInstr = T / 8;                                 // 1 KB pieces per slab
-  static constexpr int kPer = kInstr >= NW ? kInstr / NW : 1;          // pieces per wave (repeated ones when
-                                                                       // there are fewer pieces than waves)
-  const char* base;       // slab 0 of the tile
+  static constexpr int kInstr = T * kSlabBytes / 1024;                 // 1 KB pieces per slab
+  static constexpr int kPer = (kInstr + NW - 1) / NW;                  // pieces per wave (some twice where
+                                                                       // they do not divide evenly)
+  const char* base;       // the next slab to bring in
   int64_t step;           // bytes from slab to slab
   uint32_t voff[kPer];    // this lane's offset in each piece
   int where[kPer];        // its place along the summed index: byte within the slab (direct), row (transposed)
+  uint64_t lanes[kSkip ? kPer : 1];
 
   // ld: bytes from row to row; limit: valid rows (direct) or valid 16-byte
   // chunks of a row (transposed) counted from the tile's first one.
   __device__ __forceinline__ void init(const void* p, int64_t ld, int limit, int wave, int lane) {
-    base = static_cast<const char*>(p);
+    base = uniform_ptr(p);
     step = kTrans ? ld * kSlabRows : kSlabBytes;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int q = ((wave + j * NW) % kInstr) * 64 + lane;   // 16-byte position in the tile
       if constexpr (!kTrans) {
-        const int row = q >> 3;
-        const int c = direct_pos(row, q & 7);                 // an XOR is its own inverse
+        const int row = q / (kSlabBytes / 16);
+        const int c = direct_pos(row, q % (kSlabBytes / 16));   // an XOR is its own inverse
         voff[j] = static_cast<uint32_t>(min(row, limit - 1) * ld) + c * 16;
         where[j] = c * 16;
+        if constexpr (kSkip) lanes[j] = __ballot(row < limit);
       } else {
         const int row = q / (T / 8);
         const int pos = q % (T / 8);
@@ -230,146 +259,303 @@ struct Loader {
     }
   }
 
-  __device__ __forceinline__ void full(int slab, uint32_t lds, int wave) const {
-    const char* b = base + slab * step;
+  __device__ __forceinline__ void full(uint32_t lds, int wave) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) dma16_off(b, voff[j], lds + ((wave + j * NW) % kInstr) * 1024);
+    for (int j = 0; j < kPer; ++j) {
+      const uint32_t to = lds + ((wave + j * NW) % kInstr) * 1024;
+      if constexpr (kSkip)
+        dma16_off_lanes(base, voff[j], lanes[j], to);
+      else
+        dma16_off(base, voff[j], to);
+    }
+    base += step;
   }
 
   // The last slab: `left` is what remains of the summed index, in bytes
   // (direct) or rows (transposed).
-  __device__ __forceinline__ void tail(int slab, int left, uint32_t lds, int wave) const {
-    const char* b = base + slab * step;
+  __device__ __forceinline__ void tail(int left, uint32_t lds, int wave) const {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const void* src = where[j] < left ? static_cast<const void*>(b + voff[j]) : static_cast<const void*>(zero_page);
+      const void* src =
+          where[j] < left ? static_cast<const void*>(base + voff[j]) : static_cast<const void*>(zero_page);
       dma16(src, lds + ((wave + j * NW) % kInstr) * 1024);
     }
   }
 };
 
-// A lane's operand of one matrix step (step t of a slab) for the 16 tile rows
-// (direct) or columns (transposed) from i0 on.
-template <int T, bool kTrans, bool kFp4>
-__device__ __forceinline__ uint4 fragment(const unsigned char* tile, int i0, int t, int lane) {
-  const int g = lane >> 4;
-  if constexpr (!kTrans) {
-    const int row = i0 + (lane & 15);
-    // 16-bit: the four lane groups take the step's 64 bytes in order. MXFP4:
-    // group g takes blocks 2g and 2g + 1 of the slab, so that its two scales
-    // are neighbours.
-    const int c = kFp4 ? 2 * g + t : 4 * t + g;
-    return *reinterpret_cast<const uint4*>(tile + row * kSlabBytes + direct_pos(row, c) * 16);
-  } else {
-    const int i = lane & 15;
-    uint2 h[2];
+typedef __attribute__((address_space(3))) const unsigned char* LdsPtr;
+
+// This lane's operands of the matrix steps from M groups of 16 tile rows
+// (direct) or columns (transposed) of a tile of width T: group `first` and
+// every kStride-th after it. MXFP4: lane group g of a wave takes blocks 2g and
+// 2g + 1 of a slab, so that its exponents are neighbours.
+template <int T, int M, int kStride, bool kTrans, bool kFp4>
+struct Reader {
+  // Offset in the tile: of each step's first group, the others following
+  // (direct), or of the first step's groups (transposed).
+  uint32_t at[kTrans ? M : kSteps];
+
+  __device__ __forceinline__ void init(int first, int lane) {
+    const int g = lane >> 4, i = lane & 15;
+    if constexpr (!kTrans) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int row = 32 * t + 8 * g + 4 * k + (i >> 2);
-      const unsigned char* p = tile + row * (2 * T) + trans_unit<T>(row, i0 >> 4) * 32 + (i & 3) * 8;
-      const shortx4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) shortx4*)p);
-      h[k] = __builtin_bit_cast(uint2, v);
+      for (int q = 0; q < kSteps; ++q)
+        at[q] = (first * 16 + i) * kSlabBytes + direct_pos(i, kFp4 ? kSteps * g + q : 4 * q + g) * 16;
+    } else {
+      const int row = 8 * g + (i >> 2);
+#pragma unroll
+      for (int m = 0; m < M; ++m) at[m] = row * (2 * T) + trans_unit<T>(row, first + m * kStride) * 32 + (i & 3) * 8;
     }
-    return make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
   }
-}
 
-// Waits until at most `later` slabs' loads of this wave are in flight.
-template <int kPerSlab, int S>
-__device__ __forceinline__ void wait_slab(int later) {
-  if (S >= 4 && later >= 2)
-    wait_vm<2 * kPerSlab>();
-  else if (S >= 3 && later >= 1)
-    wait_vm<kPerSlab>();
-  else
+  __device__ __forceinline__ uint4 get(LdsPtr tile, int q, int m) const {
+    if constexpr (!kTrans) {
+      const u32x4 v = *reinterpret_cast<__attribute__((address_space(3))) const u32x4*>(
+          tile + at[q] + m * kStride * 16 * kSlabBytes);
+      return make_uint4(v.x, v.y, v.z, v.w);
+    } else {
+      // Rows row .. row + 3 and, four further (the same units), row + 4 .. row + 7.
+      LdsPtr p = tile + at[m] + q * 32 * 2 * T;
+      const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) shortx4*)p);
+      const shortx4 hi =
+          __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) shortx4*)(p + 4 * 2 * T));
+      const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
+      return make_uint4(l.x, l.y, h.x, h.y);
+    }
+  }
+};
+
+// One exponent byte per lane to the dword at lds_base + 4 * lane, and four
+// (one aligned word) likewise.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma1(const void* src, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, off"
+               :
+               : "v"(src), "s"(lds_base)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(const void* src, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+               :
+               : "v"(src), "s"(lds_base)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// Exponents of a slab (eight blocks per row) of the A and then the B tile's
+// rows, [row][block]. Where K is a multiple of 128 four bytes of a row are one
+// aligned word and arrive as such; otherwise each comes by itself and takes a
+// word. Blocks past K repeat earlier ones of their row (their codes are zeros,
+// and a NaN there is a NaN of that row already).
+template <int TA, int TB, int NW, bool kWords>
+struct ScaleLoader {
+  static constexpr int kBlocks = 4 * kSteps;                           // per row and slab
+  static constexpr int kWordsPerRow = kWords ? kSteps : kBlocks;
+  static constexpr int kRows = 64 / kWordsPerRow;                      // rows per piece
+  static constexpr int kInstr = (TA + TB + kRows - 1) / kRows;         // pieces per slab
+  static constexpr int kPer = (kInstr + NW - 1) / NW;
+  static constexpr int kBytes = kInstr * 256;
+  const uint8_t* src[kPer];
+  int block;              // first block of this lane's next word
+
+  __device__ __forceinline__ void init(const uint8_t* a, int a_rows, const uint8_t* b, int b_rows, int per_row, int wave,
+                                       int lane) {
+    block = (lane % kWordsPerRow) * (kWords ? 4 : 1);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int row = ((wave + j * NW) % kInstr) * kRows + lane / kWordsPerRow;
+      src[j] = row < TA ? a + int64_t(min(row, a_rows - 1)) * per_row : b + int64_t(min(row - TA, b_rows - 1)) * per_row;
+    }
+  }
+
+  __device__ __forceinline__ void load(int per_row, uint32_t lds, int wave) {
+    const int at = min(block, per_row - (kWords ? 4 : 1));
+    block += kBlocks;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint32_t to = lds + ((wave + j * NW) % kInstr) * 256;
+      if constexpr (kWords)
+        dma4(src[j] + at, to);
+      else
+        dma1(src[j] + at, to);
+    }
+  }
+
+  // The exponents of blocks 2g and 2g + 1 (g = lane >> 4) of tile row `row` (A's rows first).
+  static __device__ __forceinline__ uint32_t read(LdsPtr scales, int row, int lane) {
+    static_assert(kSteps == 2, "a lane group's blocks of a slab are a pair");
+    if constexpr (kWords) {
+      return *reinterpret_cast<__attribute__((address_space(3))) const uint16_t*>(scales + row * 8 + 2 * (lane >> 4));
+    } else {
+      LdsPtr p = scales + (row * 8 + 2 * (lane >> 4)) * 4;
+      return uint32_t(p[0]) | uint32_t(p[4]) << 8;
+    }
+  }
+};
+
+struct NoScales {
+  static constexpr int kPer = 0, kBytes = 0;
+};
+
+// Waits until at most `later` (<= L) slabs' loads of this wave are in flight.
+// Loads return in order among themselves, so other operations in flight only
+// make the wait longer.
+template <int kPerSlab, int L>
+__device__ __forceinline__ void wait_slabs(int later) {
+  if constexpr (L == 0) {
     wait_vm<0>();
-}
-
-__device__ __forceinline__ void store4(void* out, int64_t i, const floatx4& v, int dtype) {
-  if (dtype == MOE_DTYPE_F32) {
-    *reinterpret_cast<floatx4*>(static_cast<float*>(out) + i) = v;
-  } else if (dtype == MOE_DTYPE_BF16) {
-    const bf16x4 h = __builtin_convertvector(v, bf16x4);
-    *reinterpret_cast<bf16x4*>(static_cast<uint16_t*>(out) + i) = h;
   } else {
-    const halfx4 h = __builtin_convertvector(v, halfx4);
-    *reinterpret_cast<halfx4*>(static_cast<uint16_t*>(out) + i) = h;
+    if (later >= L)
+      wait_vm<kPerSlab * L>();
+    else
+      wait_slabs<kPerSlab, L - 1>(later);
   }
 }
 
-template <int TA, int TB, int S, bool kFp4>
-constexpr int ring_bytes() {
-  return S * (TA + TB) * (kSlabBytes + (kFp4 ? 8 : 0));
+__device__ __forceinline__ uint2 pack16(const floatx4& v, int dtype) {
+  return dtype == MOE_DTYPE_BF16 ? __builtin_bit_cast(uint2, __builtin_convertvector(v, bf16x4))
+                                 : __builtin_bit_cast(uint2, __builtin_convertvector(v, halfx4));
 }
+
+// Writes the M results of a lane's output row (four consecutive columns of
+// each of M groups of 16 columns from col0 on; `at`: the row's first element).
+// fp32: 16 bytes a lane, 64 contiguous ones per row and store. 16-bit: two
+// groups change halves between lanes 16 apart, so that a lane holds eight
+// consecutive columns and a store again writes 64 contiguous bytes of a row
+// (stores of 32 bytes a row took up to 1.5 times as long: they go out by line).
+template <int M, typename Get>
+__device__ __forceinline__ void store_row(void* out, int dtype, int64_t at, int col0, int cols, bool row_ok, int lane,
+                                          Get get) {
+  const int g = lane >> 4;
+  if (dtype == MOE_DTYPE_F32) {
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const int col = col0 + i * 16 + 4 * g;
+      if (row_ok && col < cols) *reinterpret_cast<floatx4*>(static_cast<float*>(out) + at + col) = get(i);
+    }
+    return;
+  }
+  uint16_t* const o = static_cast<uint16_t*>(out) + at;
+  if constexpr (M % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < M; i += 2) {
+      const uint2 p = pack16(get(i), dtype), q = pack16(get(i + 1), dtype);
+      // Lanes' rows of 16: {0, 2} of p with {1, 3} of p below them and the same of q.
+      const auto lo = __builtin_amdgcn_permlane16_swap(p.x, q.x, false, false);
+      const auto hi = __builtin_amdgcn_permlane16_swap(p.y, q.y, false, false);
+      const int col = col0 + (i + (g & 1)) * 16 + (g >> 1) * 8;
+      if (row_ok && col < cols) *reinterpret_cast<u32x4*>(o + col) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const int col = col0 + i * 16 + 4 * g;
+      if (row_ok && col < cols) *reinterpret_cast<uint2*>(o + col) = pack16(get(i), dtype);
+    }
+  }
+}
+
+template <typename T, int TA, int TB, int NW>
+struct ScalesOf {
+  using type = NoScales;
+};
+template <int TA, int TB, int NW>
+struct ScalesOf<Fp4, TA, TB, NW> {
+  using type = ScaleLoader<TA, TB, NW, true>;
+};
+template <int TA, int TB, int NW>
+struct ScalesOf<Fp4Odd, TA, TB, NW> {
+  using type = ScaleLoader<TA, TB, NW, false>;
+};
 
 template <Kind kKind, typename T, int TA, int TB, int WA, int WB, int S>
-__global__ __launch_bounds__(64 * WA * WB) void ragged_gemm(const RaggedArgs p) {
-  constexpr bool kFp4 = __is_same(T, Fp4);
+__global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2))) void ragged_gemm(const RaggedArgs p) {
+  constexpr bool kFp4 = __is_same(T, Fp4) || __is_same(T, Fp4Odd);
   constexpr bool kTransA = kKind != kForward;
   constexpr bool kTransB = kKind == kWeightGrad;
   constexpr int NW = WA * WB;
   constexpr int MA = TA / WA / 16, MB = TB / WB / 16;
-  using LA = Loader<TA, NW, kTransA>;
-  using LB = Loader<TB, NW, kTransB>;
-  constexpr int kPerSlab = LA::kPer + LB::kPer;
+  using LA = Loader<TA, NW, kTransA, false>;
+  using LB = Loader<TB, NW, kTransB, !kTransB>;
+  using LS = typename ScalesOf<T, TA, TB, NW>::type;
+  constexpr int kPerSlab = LA::kPer + LB::kPer + LS::kPer;
+  constexpr int kSlot = (TA + TB) * kSlabBytes + LS::kBytes;    // A tile, B tile, exponents
+  static_assert(kPerSlab * (S - 1) < 64, "vmcnt holds six bits");
+  static_assert(kSteps == 2, "f[q] holds step q of a slab");
   extern __shared__ __align__(16) unsigned char lds[];
-  unsigned char* const tiles = lds;                                      // [S][A tile, B tile]
-  constexpr int kSlot = (TA + TB) * kSlabBytes;
-  unsigned char* const scales = lds + S * kSlot;                         // [S][TA + TB][8] (MXFP4)
-  const uint32_t tiles_at = lds_addr(tiles);
+  const uint32_t lds_at = lds_addr(lds);
 
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int wa = wave % WA, wb = wave / WA;
   const int E = p.E, N = p.N, K = p.K;
-  // Output extents: OA along memory; the summed extent is K, N or the expert's rows.
-  const int OA = kKind == kForward ? N : K;
+  const int OA = kKind == kForward ? N : K;              // output extent along memory
   const int NT = (OA + TA - 1) / TA;
   const int MT = kKind == kWeightGrad ? (N + TB - 1) / TB : 0;
 
-  Ranges r{};
-  int total;
-  if constexpr (kKind == kWeightGrad) {
-    total = E * NT * MT;
-  } else {
-    r = scan_ranges<TB>(p.offsets, E, p.rows, lane);
-    total = r.total * NT;
-  }
+  int* const starts = reinterpret_cast<int*>(lds + S * kSlot);
+  const Ranges r = scan_ranges<TB>(p.offsets, E, p.rows, starts, lane);
+  const int total = kKind == kWeightGrad ? E * NT * MT : r.total * NT;
+  lds_barrier();
   // Workgroups go to the eight XCDs in turn: XCD i takes the i-th eighth of
   // the tasks, so neighbouring tasks share an L2.
   const int per = (total + 7) / 8;
-  for (int t = blockIdx.x; t < 8 * per; t += gridDim.x) {
-    const int L = (t & 7) * per + (t >> 3);
-    if (L >= total) continue;
-    Task k;
-    if constexpr (kKind == kWeightGrad) {
-      k.e = L / (NT * MT);
-      const int local = L - k.e * NT * MT;
-      const int grp = local / (kGroupM * NT);
-      const int gm = min(kGroupM, MT - grp * kGroupM);
-      const int in = local - grp * kGroupM * NT;
-      k.a0 = (in / gm) * TA;
-      k.b0 = (grp * kGroupM + in % gm) * TB;
-      int top = 0;                                        // the range as scan_ranges defines it
-      for (int e = lane; e <= k.e; e += 64) top = max(top, p.offsets[e]);
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) top = max(top, __shfl_xor(top, d, kWave));
-      k.row0 = min(p.rows, uniform(top));
-      k.rows = clamp_row(p.offsets[k.e + 1], k.row0, p.rows) - k.row0;
-    } else {
-      k = find_task<TB>(r, p.offsets, E, p.rows, lane, L, NT, TA);
-    }
+  int t = blockIdx.x;
+  Task k;
+  LA a;
+  LB b;
+  LS sc;
+  int ns = 0, left = 0;        // slabs, and what the last one holds (bytes, or rows)
 
-    // Operands of the tile.
-    LA a;
-    LB b;
-    int ns, left;        // slabs, and what the last one holds (bytes, or rows)
+  // The next task of this workgroup into k, if there is one.
+  auto next = [&]() -> bool {
+    for (;; t += gridDim.x) {
+      if (t >= 8 * per) return false;
+      const int L = (t & 7) * per + (t >> 3);
+      if (L >= total) continue;
+      t += gridDim.x;
+      if constexpr (kKind == kWeightGrad) {
+        k.e = L / (NT * MT);
+        const int local = L - k.e * NT * MT;
+        const int grp = local / (kGroupM * NT);
+        const int gm = min(kGroupM, MT - grp * kGroupM);
+        const int in = local - grp * kGroupM * NT;
+        k.a0 = (in / gm) * TA;
+        k.b0 = (grp * kGroupM + in % gm) * TB;
+        k.row0 = uniform(starts[k.e]);
+        k.rows = uniform(starts[k.e + 1]) - k.row0;
+      } else {
+        k = find_task<TB>(r, starts, E, L, NT, TA);
+      }
+      return true;
+    }
+  };
+
+  // Slabs are brought in one after the other, into slots 0, 1, ..
+  auto issue = [&](bool last, int slot) {
+    const uint32_t at = lds_at + slot * kSlot;
+    if (!last) {
+      a.full(at, wave);
+      b.full(at + TA * kSlabBytes, wave);
+    } else {
+      a.tail(left, at, wave);
+      b.tail(kKind == kInputGrad ? left * 2 : left, at + TA * kSlabBytes, wave);   // dy is direct: bytes
+    }
+    if constexpr (kFp4) sc.load(K / 32, at + (TA + TB) * kSlabBytes, wave);
+  };
+
+  // Task k's operands, and its first slabs.
+  auto begin = [&]() {
     if constexpr (kKind == kForward) {
       const int64_t row_bytes = kFp4 ? K / 2 : int64_t(K) * 2;
       const int64_t x_bytes = kFp4 ? K / 2 : p.ldb * 2;
-      a.init(static_cast<const char*>(p.a) + (int64_t(k.e) * N + k.a0) * row_bytes, row_bytes, min(TA, N - k.a0), wave,
-             lane);
+      const int64_t wrow = int64_t(k.e) * N + k.a0;
+      a.init(static_cast<const char*>(p.a) + wrow * row_bytes, row_bytes, min(TA, N - k.a0), wave, lane);
       b.init(static_cast<const char*>(p.b) + k.row0 * x_bytes, x_bytes, k.rows, wave, lane);
+      if constexpr (kFp4)
+        sc.init(p.a_scale + wrow * (K / 32), min(TA, N - k.a0), p.b_scale + int64_t(k.row0) * (K / 32), k.rows, K / 32,
+                wave, lane);
       ns = static_cast<int>((row_bytes + kSlabBytes - 1) / kSlabBytes);
       left = static_cast<int>(row_bytes) - (ns - 1) * kSlabBytes;
     } else if constexpr (kKind == kInputGrad) {
@@ -384,123 +570,135 @@ __global__ __launch_bounds__(64 * WA * WB) void ragged_gemm(const RaggedArgs p) 
       ns = (k.rows + kSlabRows - 1) / kSlabRows;
       left = k.rows - (ns - 1) * kSlabRows;
     }
-    const int left_b = kKind == kInputGrad ? left * 2 : left;   // dy is direct: bytes
-    auto issue = [&](int s) {
-      const uint32_t at = tiles_at + (s % S) * kSlot;
-      if (s < ns - 1) {
-        a.full(s, at, wave);
-        b.full(s, at + TA * kSlabBytes, wave);
-      } else {
-        a.tail(s, left, at, wave);
-        b.tail(s, left_b, at + TA * kSlabBytes, wave);
-      }
-    };
-    // MXFP4 scales: each thread brings eight bytes (one slab) of a tile row.
-    constexpr int kScaleRows = kFp4 ? (TA + TB + 64 * NW - 1) / (64 * NW) : 1;
-    const uint8_t* srow[kScaleRows];
-    uint64_t sval[kScaleRows];
-    if constexpr (kFp4) {
-      const int sb = K / 32;
 #pragma unroll
-      for (int j = 0; j < kScaleRows; ++j) {
-        const int i = threadIdx.x + j * 64 * NW;
-        const int an = min(k.a0 + i, N - 1), bn = k.row0 + min(i - TA, k.rows - 1);
-        srow[j] = i < TA ? p.a_scale + (int64_t(k.e) * N + an) * sb : p.b_scale + int64_t(max(bn, k.row0)) * sb;
+    for (int s = 0; s < S; ++s)
+      if (s < ns) issue(s == ns - 1, s);
+  };
+
+  // Wave (wa, wb) takes MA neighbouring groups of 16 of the A tile and every
+  // WB-th group of the B tile, so that a tile with few rows is shared evenly.
+  // f[q]: operands of step q of a slab; exponents of two groups share a word.
+  struct Frags {
+    uint4 a[MA], b[MB];
+    uint32_t sa[(MA + 1) / 2], sb[(MB + 1) / 2];
+  };
+  Reader<TA, MA, 1, kTransA, kFp4> ra;
+  Reader<TB, MB, WB, kTransB, kFp4> rb;
+  ra.init(wa * MA, lane);
+  rb.init(wb, lane);
+  int nb = 0;              // groups of B with a row of the task, for this wave
+  Frags f[2];
+  auto read = [&](int slot, int q) {
+    const LdsPtr at = (LdsPtr)lds + slot * kSlot;
+#pragma unroll
+    for (int i = 0; i < MA; ++i) f[q].a[i] = ra.get(at, q, i);
+#pragma unroll
+    for (int j = 0; j < MB; ++j)
+      if (j < nb) f[q].b[j] = rb.get(at + TA * kSlabBytes, q, j);
+    if constexpr (kFp4) {
+      const LdsPtr st = at + (TA + TB) * kSlabBytes;
+      if (q == 0) {
+#pragma unroll
+        for (int i = 0; i < MA; ++i) {
+          const uint32_t v = LS::read(st, (wa * MA + i) * 16 + (lane & 15), lane);
+          f[0].sa[i / 2] = i % 2 ? f[0].sa[i / 2] | v << 16 : v;
+        }
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+          const uint32_t v = LS::read(st, TA + (wb + j * WB) * 16 + (lane & 15), lane);
+          f[0].sb[j / 2] = j % 2 ? f[0].sb[j / 2] | v << 16 : v;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < (MA + 1) / 2; ++i) f[1].sa[i] = f[0].sa[i];
+#pragma unroll
+        for (int j = 0; j < (MB + 1) / 2; ++j) f[1].sb[j] = f[0].sb[j];
       }
     }
-    auto load_scales = [&](int s) {
-      if constexpr (kFp4) {
-        const int n = K / 32 - s * 8;
-#pragma unroll
-        for (int j = 0; j < kScaleRows; ++j) {
-          if (n >= 8) {
-            __builtin_memcpy(&sval[j], srow[j] + s * 8, 8);
-          } else {
-            uint64_t v = 0;
-            for (int i = 0; i < 8; ++i) v |= uint64_t(i < n ? srow[j][s * 8 + i] : 127) << (8 * i);
-            sval[j] = v;
-          }
-        }
-      }
-    };
-    auto keep_scales = [&](int s) {
-      if constexpr (kFp4) {
-#pragma unroll
-        for (int j = 0; j < kScaleRows; ++j) {
-          const int i = threadIdx.x + j * 64 * NW;
-          if (i < TA + TB) *reinterpret_cast<uint64_t*>(scales + ((s % S) * (TA + TB) + i) * 8) = sval[j];
-        }
-      }
-    };
+  };
 
+  bool have = next();
+  if (have) begin();
+  while (have) {
     floatx4 acc[MA][MB];
 #pragma unroll
     for (int i = 0; i < MA; ++i)
 #pragma unroll
       for (int j = 0; j < MB; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-
-    lds_barrier();      // every wave is done with the ring of the task before
-    wait_vm<0>();
+    // The compiler keeps the order of these blocks: it would sink the next
+    // step's reads to their first use otherwise.
+    auto multiply = [&](int q) {
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int s = 0; s < S - 1; ++s) {
-      if (s < ns) {
-        load_scales(s);
-        issue(s);
-        keep_scales(s);
-      }
-    }
-    for (int s = 0; s < ns; ++s) {
-      wait_slab<kPerSlab, S>(min(S - 2, ns - 1 - s));
-      lds_barrier();    // slab s is whole, and slab s - 1 has been read by every wave
-      const bool more = s + S - 1 < ns;
-      if (more) {
-        load_scales(s + S - 1);
-        issue(s + S - 1);
-      }
-      const unsigned char* const at = tiles + (s % S) * kSlot;
-      const unsigned char* const bt = at + TA * kSlabBytes;
-      int sa[MA], sb[MB];
-      if constexpr (kFp4) {
-        const unsigned char* sc = scales + (s % S) * (TA + TB) * 8;
+      for (int j = 0; j < MB; ++j) {
+        if (j < nb) {
 #pragma unroll
-        for (int i = 0; i < MA; ++i)
-          sa[i] = *reinterpret_cast<const uint16_t*>(sc + ((wa * MA + i) * 16 + (lane & 15)) * 8 + 2 * (lane >> 4));
-#pragma unroll
-        for (int j = 0; j < MB; ++j)
-          sb[j] = *reinterpret_cast<const uint16_t*>(sc + (TA + (wb * MB + j) * 16 + (lane & 15)) * 8 + 2 * (lane >> 4));
-      }
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint4 av[MA], bv[MB];
-#pragma unroll
-        for (int i = 0; i < MA; ++i) av[i] = fragment<TA, kTransA, kFp4>(at, (wa * MA + i) * 16, q, lane);
-#pragma unroll
-        for (int j = 0; j < MB; ++j) bv[j] = fragment<TB, kTransB, kFp4>(bt, (wb * MB + j) * 16, q, lane);
-#pragma unroll
-        for (int i = 0; i < MA; ++i)
-#pragma unroll
-          for (int j = 0; j < MB; ++j) {
+          for (int i = 0; i < MA; ++i) {
             if constexpr (kFp4)
-              acc[i][j] = q == 0 ? mfma_step_fp4<0>(av[i], bv[j], acc[i][j], sa[i], sb[j])
-                                 : mfma_step_fp4<1>(av[i], bv[j], acc[i][j], sa[i], sb[j]);
+              acc[i][j] = mfma_step_fp4(f[q].a[i], f[q].b[j], acc[i][j], f[q].sa[i / 2], i % 2 * 2 + q, f[q].sb[j / 2],
+                                        j % 2 * 2 + q);
             else
-              acc[i][j] = mfma_step<T>(av[i], bv[j], acc[i][j]);
+              acc[i][j] = mfma_step<T>(f[q].a[i], f[q].b[j], acc[i][j]);
           }
+        }
       }
-      if (more) keep_scales(s + S - 1);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    {
+      const int groups = ((kKind == kWeightGrad ? min(TB, N - k.b0) : k.rows) + 15) / 16;
+      nb = uniform(max(0, (groups - wb + WB - 1) / WB));
+    }
+    // The next step is read into registers while this one is multiplied.
+    // Behind a slab's barrier every wave has read that slab, and its slot takes
+    // the one S further. Slabs go through the ring in groups of S, so that
+    // slots are constants.
+    if (ns > 0) {
+      wait_slabs<kPerSlab, S - 1>(min(S - 1, ns - 1));
+      lds_barrier();
+      read(0, 0);
+      int s = 0;
+      for (; s + 2 * S < ns; s += S) {       // every slab brought in here is whole
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          read(i, 1);
+          multiply(0);
+          wait_vm<kPerSlab * (S - 2)>();
+          lds_barrier();
+          issue(false, i);
+          read((i + 1) % S, 0);
+          multiply(1);
+        }
+      }
+      for (; s < ns; s += S) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          if (s + i < ns) {
+            read(i, 1);
+            multiply(0);
+            if (s + i + 1 < ns) {
+              wait_slabs<kPerSlab, S - 2>(min(S - 2, ns - 2 - s - i));
+              lds_barrier();
+              if (s + i + S < ns) issue(s + i + S == ns - 1, i);
+              read((i + 1) % S, 0);
+            }
+            multiply(1);
+          }
+        }
+      }
+    }
+    const Task done = k;
+    have = next();
+    if (have) {
+      lds_barrier();      // every wave has read the last slab
+      begin();            // the next task's loads run under this one's stores
     }
 
-    // A lane holds four consecutive columns of one output row per 16 x 16 tile.
 #pragma unroll
     for (int j = 0; j < MB; ++j) {
-      const int row = (wb * MB + j) * 16 + (lane & 15);
-      const bool row_ok = kKind == kWeightGrad ? k.b0 + row < N : row < k.rows;
-      const int64_t at = kKind == kWeightGrad ? (int64_t(k.e) * N + k.b0 + row) * K : (k.row0 + row) * p.ldo;
-#pragma unroll
-      for (int i = 0; i < MA; ++i) {
-        const int col = k.a0 + (wa * MA + i) * 16 + 4 * (lane >> 4);
-        if (row_ok && col < OA) store4(p.out, at + col, acc[i][j], p.out_dtype);
-      }
+      const int row = (wb + j * WB) * 16 + (lane & 15);
+      const bool row_ok = kKind == kWeightGrad ? done.b0 + row < N : row < done.rows;
+      const int64_t at = kKind == kWeightGrad ? (int64_t(done.e) * N + done.b0 + row) * K : (done.row0 + row) * p.ldo;
+      store_row<MA>(p.out, p.out_dtype, at, done.a0 + wa * MA * 16, OA, row_ok, lane, [&](int i) { return acc[i][j]; });
     }
   }
 }
@@ -512,8 +710,13 @@ hipError_t run(const RaggedArgs& p, hipStream_t stream) {
   const int64_t tasks = kKind == kWeightGrad
                             ? int64_t(p.E) * nt * ((p.N + TB - 1) / TB)
                             : (int64_t(p.rows) / TB + (p.E < p.rows ? p.E : p.rows)) * nt;
-  launch(ragged_gemm<kKind, T, TA, TB, WA, WB, S>, dim3(grid_for((tasks + 7) & ~int64_t(7), 0)), dim3(64 * WA * WB),
-         ring_bytes<TA, TB, S, __is_same(T, Fp4)>(), stream, p);
+  constexpr int ring = S * ((TA + TB) * kSlabBytes + ScalesOf<T, TA, TB, WA * WB>::type::kBytes);
+  const int lds = ring + (p.E + 1) * 4;
+  // As many workgroups as run at once (two waves per SIMD, and by LDS); each
+  // takes tasks in turn and loads its next one's first slabs under its stores.
+  const int at_once = kCus * (8 / (WA * WB) < kLdsPerCu / lds ? 8 / (WA * WB) : kLdsPerCu / lds);
+  launch(ragged_gemm<kKind, T, TA, TB, WA, WB, S>, dim3(grid_for((tasks + 7) & ~int64_t(7), at_once)),
+         dim3(64 * WA * WB), lds, stream, p);
   return hipGetLastError();
 }
 
@@ -525,7 +728,11 @@ hipError_t pick(const RaggedArgs& p, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_ragged_forward(const RaggedArgs& p, int dtype, hipStream_t stream) {
-  if (dtype == MOE_DTYPE_MXFP4) return pick<kForward, Fp4>(p, stream);
+  if (dtype == MOE_DTYPE_MXFP4) {
+    const bool words = p.K % 128 == 0 && reinterpret_cast<uintptr_t>(p.a_scale) % 4 == 0 &&
+                       reinterpret_cast<uintptr_t>(p.b_scale) % 4 == 0;
+    return words ? pick<kForward, Fp4>(p, stream) : pick<kForward, Fp4Odd>(p, stream);
+  }
   return dtype == MOE_DTYPE_F16 ? pick<kForward, F16>(p, stream) : pick<kForward, Bf16>(p, stream);
 }
 

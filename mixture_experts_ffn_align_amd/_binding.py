@@ -435,6 +435,10 @@ def moe_ffn_resolved_path(desc: moe_ffn_desc) -> int:
 # Products on rows grouped by expert with ragged counts, MXFP4, row offsets
 # ---------------------------------------------------------------------------
 
+# These calls take a few microseconds on the GPU for a single token, so their
+# checks are one expression per tensor; which rule failed is worked out only
+# then.
+
 _dtype_codes = {}
 
 
@@ -452,30 +456,37 @@ def _dtype_code(name, t, allowed) -> int:
     return code
 
 
+def _expect_like(name, t, dtype, shape, device):
+    """_expect for a device that is known to be a GPU."""
+    if not (getattr(t, "dtype", None) is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        _expect(name, t, dtype, shape, device)
+
+
 def _expect_rows(name, t, shape, device=None):
-    """Check a row operand: a 2-d tensor of ``shape`` on a GPU (on ``device``
-    when given) whose rows are contiguous. Returns its row stride in elements
-    (the library checks the stride's own rules)."""
+    """Check a row operand of a known dtype: a 2-d tensor of ``shape`` on a GPU
+    (on ``device`` when given) whose rows are contiguous. Returns its row stride
+    in elements (the library checks the stride's own rules)."""
+    rows, cols = shape
+    if t.shape == shape and (t.is_cuda if device is None else t.device == device):
+        ld, step = t.stride()
+        if step == 1 or cols == 1:
+            return ld if rows > 1 else -(-cols // 8) * 8
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    rows, cols = shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: rows must be contiguous, got strides {t.stride()}")
     if t.device.type != "cuda":
         raise ValueError(f"{name}: must be on a GPU, got {t.device}")
     if device is not None and t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
-    return t.stride(0) if rows > 1 else -(-cols // 8) * 8
+    raise ValueError(f"{name}: rows must be contiguous, got strides {t.stride()}")
 
 
 def _call_on(device, stream, fn, *args) -> int:
     """fn(*args, stream) with ``device`` current; ``stream`` None is the
     device's current stream."""
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    raw = getattr(stream, "cuda_stream", stream)
-    if device.index == torch.cuda.current_device():
+    index = device.index
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else getattr(stream, "cuda_stream", stream)
+    if index == torch.cuda.current_device():
         return fn(*args, raw)
     with torch.cuda.device(device):
         return fn(*args, raw)
@@ -505,11 +516,12 @@ def moe_grouped_matmul(x, w, offsets, y, stream=None, check: bool = True) -> int
     out = _dtype_code("y", y, (dt, MOE_DTYPE_F32))
     rows = x.shape[0] if x.dim() == 2 else -1
     ldx = _expect_rows("x", x, (rows, K))
-    _expect("w", w, x.dtype, (E, N, K), x.device)
-    _expect("offsets", offsets, torch.int32, (E + 1,), x.device)
-    ldy = _expect_rows("y", y, (rows, N), x.device)
+    dev = x.device
+    _expect_like("w", w, x.dtype, (E, N, K), dev)
+    _expect_like("offsets", offsets, torch.int32, (E + 1,), dev)
+    ldy = _expect_rows("y", y, (rows, N), dev)
     d = moe_grouped_matmul_desc(rows, E, N, K, dt, out)
-    st = _call_on(x.device, stream, lib().moe_grouped_matmul, ctypes.byref(d), x.data_ptr(), ldx, w.data_ptr(),
+    st = _call_on(dev, stream, lib().moe_grouped_matmul, ctypes.byref(d), x.data_ptr(), ldx, w.data_ptr(),
                   offsets.data_ptr(), y.data_ptr(), ldy)
     if check:
         _check(st, "moe_grouped_matmul")
@@ -527,11 +539,12 @@ def moe_grouped_matmul_dx(dy, w, offsets, dx, stream=None, check: bool = True) -
     out = _dtype_code("dx", dx, (dt, MOE_DTYPE_F32))
     rows = dy.shape[0] if dy.dim() == 2 else -1
     lddy = _expect_rows("dy", dy, (rows, N))
-    _expect("w", w, dy.dtype, (E, N, K), dy.device)
-    _expect("offsets", offsets, torch.int32, (E + 1,), dy.device)
-    lddx = _expect_rows("dx", dx, (rows, K), dy.device)
+    dev = dy.device
+    _expect_like("w", w, dy.dtype, (E, N, K), dev)
+    _expect_like("offsets", offsets, torch.int32, (E + 1,), dev)
+    lddx = _expect_rows("dx", dx, (rows, K), dev)
     d = moe_grouped_matmul_desc(rows, E, N, K, dt, out)
-    st = _call_on(dy.device, stream, lib().moe_grouped_matmul_dx, ctypes.byref(d), dy.data_ptr(), lddy, w.data_ptr(),
+    st = _call_on(dev, stream, lib().moe_grouped_matmul_dx, ctypes.byref(d), dy.data_ptr(), lddy, w.data_ptr(),
                   offsets.data_ptr(), dx.data_ptr(), lddx)
     if check:
         _check(st, "moe_grouped_matmul_dx")
@@ -550,13 +563,14 @@ def moe_grouped_matmul_dw(dy, x, offsets, dw, stream=None, check: bool = True) -
     out = _dtype_code("dw", dw, (dt, MOE_DTYPE_F32))
     rows = dy.shape[0] if dy.dim() == 2 else -1
     lddy = _expect_rows("dy", dy, (rows, N))
+    dev = dy.device
     if x.dtype != dy.dtype:
         raise TypeError(f"x: expected dtype {dy.dtype}, got {x.dtype}")
-    ldx = _expect_rows("x", x, (rows, K), dy.device)
-    _expect("offsets", offsets, torch.int32, (E + 1,), dy.device)
-    _expect("dw", dw, dw.dtype, (E, N, K), dy.device)
+    ldx = _expect_rows("x", x, (rows, K), dev)
+    _expect_like("offsets", offsets, torch.int32, (E + 1,), dev)
+    _expect_like("dw", dw, dw.dtype, (E, N, K), dev)
     d = moe_grouped_matmul_desc(rows, E, N, K, dt, out)
-    st = _call_on(dy.device, stream, lib().moe_grouped_matmul_dw, ctypes.byref(d), dy.data_ptr(), lddy, x.data_ptr(),
+    st = _call_on(dev, stream, lib().moe_grouped_matmul_dw, ctypes.byref(d), dy.data_ptr(), lddy, x.data_ptr(),
                   ldx, offsets.data_ptr(), dw.data_ptr())
     if check:
         _check(st, "moe_grouped_matmul_dw")
@@ -572,12 +586,16 @@ def moe_grouped_matmul_mxfp4(xq, x_scale, wq, w_scale, offsets, y, stream=None, 
     E, N, half = _expect_3d("wq", wq)
     K = 2 * half
     out = _dtype_code("y", y, _ALL_TYPES)
-    rows = xq.shape[0]
-    dev = _expect("xq", xq, torch.uint8, (rows, half))
-    _expect("x_scale", x_scale, torch.uint8, (rows, K // 32), dev)
-    _expect("wq", wq, torch.uint8, (E, N, half), dev)
-    _expect("w_scale", w_scale, torch.uint8, (E, N, K // 32), dev)
-    _expect("offsets", offsets, torch.int32, (E + 1,), dev)
+    if not hasattr(xq, "data_ptr"):
+        raise TypeError(f"xq: expected a torch.Tensor, got {type(xq).__name__}")
+    rows = xq.shape[0] if xq.dim() == 2 else -1
+    dev = xq.device
+    if not (xq.is_cuda and xq.dtype is torch.uint8 and xq.shape == (rows, half) and xq.is_contiguous()):
+        _expect("xq", xq, torch.uint8, (rows, half))
+    _expect_like("x_scale", x_scale, torch.uint8, (rows, K // 32), dev)
+    _expect_like("wq", wq, torch.uint8, (E, N, half), dev)
+    _expect_like("w_scale", w_scale, torch.uint8, (E, N, K // 32), dev)
+    _expect_like("offsets", offsets, torch.int32, (E + 1,), dev)
     ldy = _expect_rows("y", y, (rows, N), dev)
     d = moe_grouped_matmul_desc(rows, E, N, K, MOE_DTYPE_MXFP4, out)
     st = _call_on(dev, stream, lib().moe_grouped_matmul_mxfp4, ctypes.byref(d), xq.data_ptr(), x_scale.data_ptr(),
@@ -593,17 +611,18 @@ def _mxfp4_rows(name, t, q, scale):
     import torch
     if t.dim() < 2:
         raise ValueError(f"{name}: expected [.., K], got shape {tuple(t.shape)}")
-    lead, K = tuple(t.shape[:-1]), t.shape[-1]
-    if t.dim() == 2:
-        ld = _expect_rows(name, t, (lead[0], K))
+    *lead, K = t.shape
+    if len(lead) == 1:
+        rows = lead[0]
+        ld = _expect_rows(name, t, (rows, K))
     else:
         _expect(name, t, t.dtype, t.shape)
-        ld = K
-    _expect("q", q, torch.uint8, lead + (K // 2,), t.device)
-    _expect("scale", scale, torch.uint8, lead + (K // 32,), t.device)
-    rows = 1
-    for n in lead:
-        rows *= n
+        ld, rows = K, 1
+        for n in lead:
+            rows *= n
+    dev = t.device
+    _expect_like("q", q, torch.uint8, (*lead, K // 2), dev)
+    _expect_like("scale", scale, torch.uint8, (*lead, K // 32), dev)
     return rows, K, ld
 
 
@@ -639,9 +658,12 @@ def moe_align_offsets(expert_block_ids, num_padded, E: int, b: int, offsets, str
     if not hasattr(expert_block_ids, "data_ptr"):
         raise TypeError(f"expert_block_ids: expected a torch.Tensor, got {type(expert_block_ids).__name__}")
     n = expert_block_ids.numel()
-    dev = _expect("expert_block_ids", expert_block_ids, torch.int32, (n,))
-    _expect("num_padded", num_padded, torch.int32, (1,), dev)
-    _expect("offsets", offsets, torch.int32, (E + 1,), dev)
+    dev = expert_block_ids.device
+    if dev.type != "cuda":
+        _expect("expert_block_ids", expert_block_ids, torch.int32, (n,))
+    _expect_like("expert_block_ids", expert_block_ids, torch.int32, (n,), dev)
+    _expect_like("num_padded", num_padded, torch.int32, (1,), dev)
+    _expect_like("offsets", offsets, torch.int32, (E + 1,), dev)
     st = _call_on(dev, stream, lib().moe_align_offsets, expert_block_ids.data_ptr(), num_padded.data_ptr(), n, E, b,
                   offsets.data_ptr())
     if check:

@@ -65,16 +65,6 @@ __device__ __forceinline__ void dma16_off(const void* base, uint32_t voff, uint3
                : "v"(voff), "s"(base), "s"(lds_base)
                : "memory", "m0");
 }
-
-// The same for the lanes in `lanes` only (all 64 are active before and after).
-// With none it still counts as one load, so waits by count stay right.
-__device__ __forceinline__ void dma16_off_lanes(const void* base, uint32_t voff, uint64_t lanes, uint32_t lds_base) {
-  asm volatile(
-      "s_mov_b32 m0, %2\n\ts_mov_b64 exec, %3\n\tglobal_load_lds_dwordx4 %0, %1\n\ts_mov_b64 exec, -1"
-      :
-      : "v"(voff), "s"(base), "s"(lds_base), "s"(lanes)
-      : "memory", "m0");
-}
 #pragma clang diagnostic pop
 
 // A wave-uniform address made explicitly scalar.
@@ -114,6 +104,19 @@ __device__ __forceinline__ floatx4 mfma_step_fp4(const uint4& a, const uint4& b,
 
 __device__ __forceinline__ int clamp_row(int v, int lo, int rows) { return min(rows, max(lo, v)); }
 
+// Inclusive scan over the wave's lanes of values >= 0 under an operation for
+// which 0 is neutral: within rows of 16 lanes, then across them.
+template <typename Op>
+__device__ __forceinline__ int wave_scan(int v, Op op) {
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false));   // row_shr 1, 2, 4, 8
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false));
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false));
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false));
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));   // row_bcast 15 into rows 1 and 3
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));   // row_bcast 31 into rows 2 and 3
+  return v;
+}
+
 // Row tiles of the experts, by lane: lane l holds ceil(E / 64) consecutive ones.
 struct Ranges {
   int first;   // first expert of this lane
@@ -128,33 +131,32 @@ struct Ranges {
 // wave scans (and stores the same values); the caller puts a barrier behind.
 template <int TB>
 __device__ __forceinline__ Ranges scan_ranges(const int32_t* offsets, int E, int rows, int* starts, int lane) {
+  constexpr int kHeld = 4;     // offsets a lane keeps in registers (up to 256 experts): one round trip
   const int per = (E + 63) / 64;
   Ranges r;
   r.first = min(E, lane * per);
   const int last = min(E, r.first + per);
-  int top = 0;
-  for (int e = r.first; e < last; ++e) top = max(top, offsets[e]);
+  int held[kHeld + 1];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(top, d, kWave);
-    if (lane >= d) top = max(top, o);
-  }
-  const int before = __shfl_up(top, 1, kWave);
-  int cur = r.first < E ? clamp_row(offsets[r.first], lane == 0 ? 0 : before, rows) : rows;
+  for (int i = 0; i <= kHeld; ++i) held[i] = offsets[min(E, r.first + i)];
+  auto offset = [&](int e) {
+    const int i = e - r.first;
+    return i == 0 ? held[0] : i == 1 ? held[1] : i == 2 ? held[2] : i == 3 ? held[3] : i == 4 ? held[4] : offsets[e];
+  };
+  int top = 0;
+  for (int e = r.first; e < last; ++e) top = max(top, offset(e));
+  top = wave_scan(top, [](int a, int b) { return max(a, b); });
+  const int before = __builtin_amdgcn_update_dpp(0, top, 0x138, 0xF, 0xF, false);   // the lane below's; 0 for lane 0
+  int cur = r.first < E ? clamp_row(offset(r.first), before, rows) : rows;
   int tiles = 0;
   for (int e = r.first; e < last; ++e) {
-    const int nxt = clamp_row(offsets[e + 1], cur, rows);
+    const int nxt = clamp_row(offset(e + 1), cur, rows);
     starts[e] = cur;
     if (e + 1 == E) starts[E] = nxt;
     tiles += (nxt - cur + TB - 1) / TB;
     cur = nxt;
   }
-  int incl = tiles;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(incl, d, kWave);
-    if (lane >= d) incl += o;
-  }
+  const int incl = wave_scan(tiles, [](int a, int b) { return a + b; });
   r.tiles = tiles;
   r.base = incl - tiles;
   r.total = __builtin_amdgcn_readlane(incl, 63);
@@ -222,24 +224,27 @@ __device__ __forceinline__ int trans_unit(int row, int u) {
 
 // One operand's side of the data movement: which bytes this wave brings in.
 // kTrans: the tile is [64 rows][T] (the rows are the summed index).
-// kSkip (direct): rows past the limit are left out, so their LDS holds whatever
-// was there (it only reaches outputs that are not stored).
+// kSkip (direct): pieces without a valid row are left out; their LDS then holds
+// whatever was there, which only reaches outputs that are not stored.
 template <int T, int NW, bool kTrans, bool kSkip>
 struct Loader {
   static constexpr int kInstr = T * kSlabBytes / 1024;                 // 1 KB pieces per slab
   static constexpr int kPer = (kInstr + NW - 1) / NW;                  // pieces per wave (some twice where
                                                                        // they do not divide evenly)
+  static constexpr int kPieceRows = 1024 / kSlabBytes;                 // (direct)
+  static_assert(!kSkip || kInstr % NW == 0, "pieces in row order, each once");
   const char* base;       // the next slab to bring in
   int64_t step;           // bytes from slab to slab
   uint32_t voff[kPer];    // this lane's offset in each piece
   int where[kPer];        // its place along the summed index: byte within the slab (direct), row (transposed)
-  uint64_t lanes[kSkip ? kPer : 1];
+  int have;               // kSkip: valid rows from this wave's first piece on
 
   // ld: bytes from row to row; limit: valid rows (direct) or valid 16-byte
   // chunks of a row (transposed) counted from the tile's first one.
   __device__ __forceinline__ void init(const void* p, int64_t ld, int limit, int wave, int lane) {
     base = uniform_ptr(p);
     step = kTrans ? ld * kSlabRows : kSlabBytes;
+    have = uniform(limit - wave * kPieceRows);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int q = ((wave + j * NW) % kInstr) * 64 + lane;   // 16-byte position in the tile
@@ -248,7 +253,6 @@ struct Loader {
         const int c = direct_pos(row, q % (kSlabBytes / 16));   // an XOR is its own inverse
         voff[j] = static_cast<uint32_t>(min(row, limit - 1) * ld) + c * 16;
         where[j] = c * 16;
-        if constexpr (kSkip) lanes[j] = __ballot(row < limit);
       } else {
         const int row = q / (T / 8);
         const int pos = q % (T / 8);
@@ -262,11 +266,8 @@ struct Loader {
   __device__ __forceinline__ void full(uint32_t lds, int wave) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const uint32_t to = lds + ((wave + j * NW) % kInstr) * 1024;
-      if constexpr (kSkip)
-        dma16_off_lanes(base, voff[j], lanes[j], to);
-      else
-        dma16_off(base, voff[j], to);
+      if (kSkip && have <= j * NW * kPieceRows) break;
+      dma16_off(base, voff[j], lds + ((wave + j * NW) % kInstr) * 1024);
     }
     base += step;
   }
@@ -477,12 +478,14 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
   constexpr int NW = WA * WB;
   constexpr int MA = TA / WA / 16, MB = TB / WB / 16;
   using LA = Loader<TA, NW, kTransA, false>;
-  using LB = Loader<TB, NW, kTransB, !kTransB>;
+  // With a ring of two every wait is for all loads, so some may be left out.
+  constexpr bool kSkipB = !kTransB && S == 2 && TB / 8 % NW == 0;
+  using LB = Loader<TB, NW, kTransB, kSkipB>;
   using LS = typename ScalesOf<T, TA, TB, NW>::type;
   constexpr int kPerSlab = LA::kPer + LB::kPer + LS::kPer;
   constexpr int kSlot = (TA + TB) * kSlabBytes + LS::kBytes;    // A tile, B tile, exponents
   static_assert(kPerSlab * (S - 1) < 64, "vmcnt holds six bits");
-  static_assert(kSteps == 2, "f[q] holds step q of a slab");
+  static_assert(kSteps == 2, "fb[q] holds step q of a slab");
   extern __shared__ __align__(16) unsigned char lds[];
   const uint32_t lds_at = lds_addr(lds);
 
@@ -577,42 +580,42 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
 
   // Wave (wa, wb) takes MA neighbouring groups of 16 of the A tile and every
   // WB-th group of the B tile, so that a tile with few rows is shared evenly.
-  // f[q]: operands of step q of a slab; exponents of two groups share a word.
-  struct Frags {
-    uint4 a[MA], b[MB];
-    uint32_t sa[(MA + 1) / 2], sb[(MB + 1) / 2];
-  };
+  // A matrix step's A operands are read in kHalves parts (two where all of
+  // them would not fit the registers beside the sums).
+  constexpr int kHalves = MA >= 8 ? 2 : 1;
+  constexpr int kPart = MA / kHalves;
   Reader<TA, MA, 1, kTransA, kFp4> ra;
   Reader<TB, MB, WB, kTransB, kFp4> rb;
   ra.init(wa * MA, lane);
   rb.init(wb, lane);
   int nb = 0;              // groups of B with a row of the task, for this wave
-  Frags f[2];
-  auto read = [&](int slot, int q) {
+  uint4 fa[2][kPart], fb[2][MB];
+  struct {
+    uint32_t a[(MA + 1) / 2], b[(MB + 1) / 2];   // exponents of two groups share a word
+  } now, then;
+  // Part h of step q of the slab in `slot`.
+  auto read = [&](int slot, int q, int h) {
     const LdsPtr at = (LdsPtr)lds + slot * kSlot;
 #pragma unroll
-    for (int i = 0; i < MA; ++i) f[q].a[i] = ra.get(at, q, i);
+    for (int i = 0; i < kPart; ++i) fa[(q * kHalves + h) % 2][i] = ra.get(at, q, h * kPart + i);
+    if (h == 0) {
 #pragma unroll
-    for (int j = 0; j < MB; ++j)
-      if (j < nb) f[q].b[j] = rb.get(at + TA * kSlabBytes, q, j);
+      for (int j = 0; j < MB; ++j)
+        if (j < nb) fb[q][j] = rb.get(at + TA * kSlabBytes, q, j);
+    }
     if constexpr (kFp4) {
-      const LdsPtr st = at + (TA + TB) * kSlabBytes;
-      if (q == 0) {
+      if (q == 0 && h == 0) {
+        const LdsPtr st = at + (TA + TB) * kSlabBytes;
 #pragma unroll
         for (int i = 0; i < MA; ++i) {
           const uint32_t v = LS::read(st, (wa * MA + i) * 16 + (lane & 15), lane);
-          f[0].sa[i / 2] = i % 2 ? f[0].sa[i / 2] | v << 16 : v;
+          then.a[i / 2] = i % 2 ? then.a[i / 2] | v << 16 : v;
         }
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
           const uint32_t v = LS::read(st, TA + (wb + j * WB) * 16 + (lane & 15), lane);
-          f[0].sb[j / 2] = j % 2 ? f[0].sb[j / 2] | v << 16 : v;
+          then.b[j / 2] = j % 2 ? then.b[j / 2] | v << 16 : v;
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < (MA + 1) / 2; ++i) f[1].sa[i] = f[0].sa[i];
-#pragma unroll
-        for (int j = 0; j < (MB + 1) / 2; ++j) f[1].sb[j] = f[0].sb[j];
       }
     }
   };
@@ -626,62 +629,72 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
 #pragma unroll
       for (int j = 0; j < MB; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
     // The compiler keeps the order of these blocks: it would sink the next
-    // step's reads to their first use otherwise.
-    auto multiply = [&](int q) {
+    // part's reads to their first use otherwise.
+    auto multiply = [&](int q, int h) {
+      if constexpr (kFp4) {
+        if (q == 0 && h == 0) now = then;
+      }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < MB; ++j) {
         if (j < nb) {
 #pragma unroll
-          for (int i = 0; i < MA; ++i) {
+          for (int n = 0; n < kPart; ++n) {
+            const int i = h * kPart + n;
+            const uint4& av = fa[(q * kHalves + h) % 2][n];
             if constexpr (kFp4)
-              acc[i][j] = mfma_step_fp4(f[q].a[i], f[q].b[j], acc[i][j], f[q].sa[i / 2], i % 2 * 2 + q, f[q].sb[j / 2],
-                                        j % 2 * 2 + q);
+              acc[i][j] = mfma_step_fp4(av, fb[q][j], acc[i][j], now.a[i / 2], i % 2 * 2 + q, now.b[j / 2], j % 2 * 2 + q);
             else
-              acc[i][j] = mfma_step<T>(f[q].a[i], f[q].b[j], acc[i][j]);
+              acc[i][j] = mfma_step<T>(av, fb[q][j], acc[i][j]);
           }
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     };
+    // The parts of the slab in slot i but the last product.
+    auto inside = [&](int i) {
+#pragma unroll
+      for (int n = 1; n < 2 * kHalves; ++n) {
+        read(i, n / kHalves, n % kHalves);
+        multiply((n - 1) / kHalves, (n - 1) % kHalves);
+      }
+    };
     {
       const int groups = ((kKind == kWeightGrad ? min(TB, N - k.b0) : k.rows) + 15) / 16;
       nb = uniform(max(0, (groups - wb + WB - 1) / WB));
     }
-    // The next step is read into registers while this one is multiplied.
+    // The next part is read into registers while this one is multiplied.
     // Behind a slab's barrier every wave has read that slab, and its slot takes
     // the one S further. Slabs go through the ring in groups of S, so that
     // slots are constants.
     if (ns > 0) {
-      wait_slabs<kPerSlab, S - 1>(min(S - 1, ns - 1));
+      wait_slabs<kPerSlab, S - 1>(kSkipB ? 0 : min(S - 1, ns - 1));
       lds_barrier();
-      read(0, 0);
+      read(0, 0, 0);
       int s = 0;
       for (; s + 2 * S < ns; s += S) {       // every slab brought in here is whole
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-          read(i, 1);
-          multiply(0);
+          inside(i);
           wait_vm<kPerSlab * (S - 2)>();
           lds_barrier();
           issue(false, i);
-          read((i + 1) % S, 0);
-          multiply(1);
+          read((i + 1) % S, 0, 0);
+          multiply(1, kHalves - 1);
         }
       }
       for (; s < ns; s += S) {
 #pragma unroll
         for (int i = 0; i < S; ++i) {
           if (s + i < ns) {
-            read(i, 1);
-            multiply(0);
+            inside(i);
             if (s + i + 1 < ns) {
               wait_slabs<kPerSlab, S - 2>(min(S - 2, ns - 2 - s - i));
               lds_barrier();
               if (s + i + S < ns) issue(s + i + S == ns - 1, i);
-              read((i + 1) % S, 0);
+              read((i + 1) % S, 0, 0);
             }
-            multiply(1);
+            multiply(1, kHalves - 1);
           }
         }
       }
@@ -703,13 +716,152 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
   }
 }
 
+// The forward product for experts with few rows each (a token's or a small
+// batch's routes): bound by reading each weight once. A workgroup owns 16 rows
+// and 16 * G output columns of an expert, and its waves share the summed
+// index, so that a single token's products spread over the chip; weights go
+// from memory straight to the matrix instructions' registers, every load of two
+// blocks in flight before the first product. The waves' sums are added in wave
+// order through LDS.
+constexpr int kStreamWaves = 4;
+constexpr int kBlockBytes = 256;      // of a row per wave and turn: four matrix steps
+
+template <typename T, int G>
+__global__ __launch_bounds__(64 * kStreamWaves) __attribute__((amdgpu_waves_per_eu(G == 1 ? 4 : 3))) void
+ragged_stream(const RaggedArgs p) {
+  constexpr bool kFp4 = __is_same(T, Fp4);
+  extern __shared__ __align__(16) unsigned char lds[];      // the waves' sums, then the experts' start rows
+  floatx4* const sums = reinterpret_cast<floatx4*>(lds);
+  int* const starts = reinterpret_cast<int*>(lds + kStreamWaves * G * 64 * sizeof(floatx4));
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int E = p.E, N = p.N, K = p.K;
+  const int NT = (N + (16 * G) - 1) / (16 * G);
+  const Ranges r = scan_ranges<16>(p.offsets, E, p.rows, starts, lane);
+  const int total = r.total * NT;
+  lds_barrier();
+  const int per = (total + 7) / 8;       // XCD i takes the i-th eighth of the tasks
+  for (int t = blockIdx.x; t < 8 * per; t += gridDim.x) {
+    const int L = (t & 7) * per + (t >> 3);
+    if (L >= total) continue;
+    const Task k = find_task<16>(r, starts, E, L, NT, (16 * G));
+    const int64_t wld = kFp4 ? K / 2 : int64_t(K) * 2, xld = kFp4 ? K / 2 : p.ldb * 2;
+    const int bytes = static_cast<int>(wld);
+    const int sb = K / 32;                // exponents of a row
+    const char* wrow[G];
+    const uint8_t* wscale[G];
+    const int64_t xr = k.row0 + min(lane & 15, k.rows - 1);
+    const char* const xrow = static_cast<const char*>(p.b) + xr * xld;
+    const uint8_t* const xscale = kFp4 ? p.b_scale + xr * sb : nullptr;
+#pragma unroll
+    for (int c = 0; c < G; ++c) {
+      const int64_t n = int64_t(k.e) * N + min(k.a0 + c * 16 + (lane & 15), N - 1);
+      wrow[c] = static_cast<const char*>(p.a) + n * wld;
+      wscale[c] = kFp4 ? p.a_scale + n * sb : nullptr;
+    }
+    floatx4 acc[G];
+#pragma unroll
+    for (int c = 0; c < G; ++c) acc[c] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+    // One block of a wave: 256 bytes of every row. 16-bit: matrix step s takes
+    // bytes 64 s .. 64 s + 63. MXFP4: lane group g takes blocks 4g .. 4g + 3 of
+    // the sixteen, one a step, so that its exponents are one word.
+    struct Block {
+      uint4 w[G][4], x[4];
+      uint32_t ws[G], xs;
+    };
+    auto chunk = [&](int s) { return kFp4 ? 64 * g + 16 * s : 64 * s + 16 * g; };
+    auto load = [&](Block& b, int at) {
+      if (at + kBlockBytes <= bytes) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          b.x[s] = *reinterpret_cast<const uint4*>(xrow + at + chunk(s));
+#pragma unroll
+          for (int c = 0; c < G; ++c) b.w[c][s] = *reinterpret_cast<const uint4*>(wrow[c] + at + chunk(s));
+        }
+        if constexpr (kFp4) {
+          __builtin_memcpy(&b.xs, xscale + at / 16 + 4 * g, 4);
+#pragma unroll
+          for (int c = 0; c < G; ++c) __builtin_memcpy(&b.ws[c], wscale[c] + at / 16 + 4 * g, 4);
+        }
+      } else {                            // the row ends inside: zeros, with the exponent of one
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const bool in = at + chunk(s) < bytes;
+          const int from = in ? at + chunk(s) : 0;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          const uint4 xv = *reinterpret_cast<const uint4*>(xrow + from);
+          b.x[s] = in ? xv : zero;
+#pragma unroll
+          for (int c = 0; c < G; ++c) {
+            const uint4 wv = *reinterpret_cast<const uint4*>(wrow[c] + from);
+            b.w[c][s] = in ? wv : zero;
+          }
+        }
+        if constexpr (kFp4) {
+          b.xs = 0;
+#pragma unroll
+          for (int c = 0; c < G; ++c) b.ws[c] = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int n = at / 16 + 4 * g + i;
+            const bool in = n < sb;
+            b.xs |= uint32_t(in ? xscale[in ? n : 0] : 127) << (8 * i);
+#pragma unroll
+            for (int c = 0; c < G; ++c) b.ws[c] |= uint32_t(in ? wscale[c][in ? n : 0] : 127) << (8 * i);
+          }
+        }
+      }
+    };
+    auto multiply = [&](const Block& b) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int c = 0; c < G; ++c) {
+          if constexpr (kFp4)
+            acc[c] = mfma_step_fp4(b.w[c][s], b.x[s], acc[c], b.ws[c], s, b.xs, s);
+          else
+            acc[c] = mfma_step<T>(b.w[c][s], b.x[s], acc[c]);
+        }
+    };
+    constexpr int kTurn = kStreamWaves * kBlockBytes;
+    for (int at = wave * kBlockBytes; at < bytes; at += 2 * kTurn) {
+      Block b0, b1;
+      load(b0, at);
+      const bool two = at + kTurn < bytes;
+      if (two) load(b1, at + kTurn);
+      multiply(b0);
+      if (two) multiply(b1);
+    }
+#pragma unroll
+    for (int c = 0; c < G; ++c) sums[(wave * G + c) * 64 + lane] = acc[c];
+    lds_barrier();
+    if (wave < G) {
+      floatx4 v = sums[wave * 64 + lane];
+#pragma unroll
+      for (int i = 1; i < kStreamWaves; ++i) {
+        const floatx4 o = sums[(i * G + wave) * 64 + lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += o[j];
+      }
+      store_row<1>(p.out, p.out_dtype, (k.row0 + (lane & 15)) * p.ldo, k.a0 + wave * 16, N, (lane & 15) < k.rows, lane,
+                   [&](int) { return v; });
+    }
+    lds_barrier();
+  }
+}
+
+int64_t row_tiles(const RaggedArgs& p, int tile) {      // at most
+  return int64_t(p.rows) / tile + (p.E < p.rows ? p.E : p.rows);
+}
+
 template <Kind kKind, typename T, int TA, int TB, int WA, int WB, int S>
 hipError_t run(const RaggedArgs& p, hipStream_t stream) {
   const int64_t OA = kKind == kForward ? p.N : p.K;
   const int64_t nt = (OA + TA - 1) / TA;
   const int64_t tasks = kKind == kWeightGrad
                             ? int64_t(p.E) * nt * ((p.N + TB - 1) / TB)
-                            : (int64_t(p.rows) / TB + (p.E < p.rows ? p.E : p.rows)) * nt;
+                            : row_tiles(p, TB) * nt;
   constexpr int ring = S * ((TA + TB) * kSlabBytes + ScalesOf<T, TA, TB, WA * WB>::type::kBytes);
   const int lds = ring + (p.E + 1) * 4;
   // As many workgroups as run at once (two waves per SIMD, and by LDS); each
@@ -718,6 +870,33 @@ hipError_t run(const RaggedArgs& p, hipStream_t stream) {
   launch(ragged_gemm<kKind, T, TA, TB, WA, WB, S>, dim3(grid_for((tasks + 7) & ~int64_t(7), at_once)),
          dim3(64 * WA * WB), lds, stream, p);
   return hipGetLastError();
+}
+
+template <typename T, int G>
+hipError_t run_stream(const RaggedArgs& p, hipStream_t stream) {
+  const int64_t tasks = row_tiles(p, 16) * ((p.N + 16 * G - 1) / (16 * G));
+  const int lds = kStreamWaves * G * 64 * int(sizeof(floatx4)) + (p.E + 1) * 4;
+  launch(ragged_stream<T, G>, dim3(grid_for((tasks + 7) & ~int64_t(7), 0)), dim3(64 * kStreamWaves), lds, stream, p);
+  return hipGetLastError();
+}
+
+// Which kernel: ragged_stream fills the chip with few rows, ragged_gemm reads
+// weights in whole 128-byte lines and shares them between the rows of a tile.
+// Measured at N = 1536, K = 2048, 128 experts, top-8 (us, stream / tiles):
+//   bf16, tokens 1: 11.8 / 20.0, 4: 37.9 / 42.2, 21: 103 / 124, 128: 143 / 150, 256: 197 / 163;
+//   MXFP4, tokens 1: 6.6 / 10.5, 4: 16.4 / 14.1, 21: 51.4 / 38.4.
+// So 16-bit operands stream up to eight rows per expert, MXFP4 (a stream's
+// loads of a quarter of the bytes leave more of each line to the cache) only
+// where the tiles would leave CUs idle.
+bool few_rows(const RaggedArgs& p) { return p.rows <= 8 * int64_t(p.E < p.rows ? p.E : p.rows); }
+bool few_tiles(const RaggedArgs& p) { return row_tiles(p, 128) * ((p.N + 127) / 128) < kCus; }
+
+// Columns per workgroup: 16 where 32 would give a CU fewer than four
+// workgroups (bf16, 1 token: 11.8 / 13.2 us; 4 tokens: 39.7 / 37.9).
+template <typename T>
+hipError_t pick_stream(const RaggedArgs& p, hipStream_t stream) {
+  if (row_tiles(p, 16) * ((p.N + 31) / 32) < 4 * kCus) return run_stream<T, 1>(p, stream);
+  return run_stream<T, 2>(p, stream);
 }
 
 template <Kind kKind, typename T>
@@ -731,8 +910,10 @@ hipError_t launch_ragged_forward(const RaggedArgs& p, int dtype, hipStream_t str
   if (dtype == MOE_DTYPE_MXFP4) {
     const bool words = p.K % 128 == 0 && reinterpret_cast<uintptr_t>(p.a_scale) % 4 == 0 &&
                        reinterpret_cast<uintptr_t>(p.b_scale) % 4 == 0;
+    if (few_rows(p) && few_tiles(p)) return run_stream<Fp4, 1>(p, stream);
     return words ? pick<kForward, Fp4>(p, stream) : pick<kForward, Fp4Odd>(p, stream);
   }
+  if (few_rows(p)) return dtype == MOE_DTYPE_F16 ? pick_stream<F16>(p, stream) : pick_stream<Bf16>(p, stream);
   return dtype == MOE_DTYPE_F16 ? pick<kForward, F16>(p, stream) : pick<kForward, Bf16>(p, stream);
 }
 

@@ -901,6 +901,9 @@ hipError_t pick_stream(const RaggedArgs& p, hipStream_t stream) {
 
 template <Kind kKind, typename T>
 hipError_t pick(const RaggedArgs& p, hipStream_t stream) {
+  if constexpr (kKind == kForward && !__is_same(T, Fp4) && !__is_same(T, Fp4Odd)) {
+    if (p.rows >= 1024 * int64_t(p.E)) return run<kKind, T, 256, 256, 2, 4, 2>(p, stream);
+  }
   return run<kKind, T, 128, 128, 2, 2, 2>(p, stream);
 }
 

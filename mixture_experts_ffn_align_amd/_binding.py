@@ -564,8 +564,7 @@ def moe_grouped_matmul_dw(dy, x, offsets, dw, stream=None, check: bool = True) -
     rows = dy.shape[0] if dy.dim() == 2 else -1
     lddy = _expect_rows("dy", dy, (rows, N))
     dev = dy.device
-    if x.dtype != dy.dtype:
-        raise TypeError(f"x: expected dtype {dy.dtype}, got {x.dtype}")
+    _dtype_code("x", x, (dt,))
     ldx = _expect_rows("x", x, (rows, K), dev)
     _expect_like("offsets", offsets, torch.int32, (E + 1,), dev)
     _expect_like("dw", dw, dw.dtype, (E, N, K), dev)

@@ -470,8 +470,14 @@ struct ScalesOf<Fp4Odd, TA, TB, NW> {
   using type = ScaleLoader<TA, TB, NW, false>;
 };
 
-template <Kind kKind, typename T, int TA, int TB, int WA, int WB, int S>
-__global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2))) void ragged_gemm(const RaggedArgs p) {
+// kSplit > 1: the summed index is shared by kSplit waves, each with a ring of
+// its own and the whole tile's sums, which are added in wave order at the end;
+// for products of few tiles, where a tile's slabs one after the other would be
+// most of the time.
+template <Kind kKind, typename T, int TA, int TB, int WA, int WB, int S, int kSplit>
+__global__ __launch_bounds__(64 * WA * WB * kSplit) __attribute__((amdgpu_waves_per_eu(2))) void
+ragged_gemm(const RaggedArgs p) {
+  static_assert(kSplit == 1 || WA * WB == 1, "waves that share the summed index keep whole tiles");
   constexpr bool kFp4 = __is_same(T, Fp4) || __is_same(T, Fp4Odd);
   constexpr bool kTransA = kKind != kForward;
   constexpr bool kTransB = kKind == kWeightGrad;
@@ -487,17 +493,26 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
   static_assert(kPerSlab * (S - 1) < 64, "vmcnt holds six bits");
   static_assert(kSteps == 2, "fb[q] holds step q of a slab");
   extern __shared__ __align__(16) unsigned char lds[];
-  const uint32_t lds_at = lds_addr(lds);
 
   const int lane = threadIdx.x & 63;
-  const int wave = uniform(threadIdx.x >> 6);
+  const int share = kSplit == 1 ? 0 : uniform(threadIdx.x >> 6);     // of the summed index
+  const int wave = kSplit == 1 ? uniform(threadIdx.x >> 6) : 0;
   const int wa = wave % WA, wb = wave / WA;
+  unsigned char* const ring = lds + share * S * kSlot;
+  const uint32_t ring_at = lds_addr(ring);
+  // What the waves of a ring wait for before a slot is read or filled again.
+  auto ring_barrier = [&]() {
+    if constexpr (kSplit == 1)
+      lds_barrier();
+    else
+      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+  };
   const int E = p.E, N = p.N, K = p.K;
   const int OA = kKind == kForward ? N : K;              // output extent along memory
   const int NT = (OA + TA - 1) / TA;
   const int MT = kKind == kWeightGrad ? (N + TB - 1) / TB : 0;
 
-  int* const starts = reinterpret_cast<int*>(lds + S * kSlot);
+  int* const starts = reinterpret_cast<int*>(lds + kSplit * S * kSlot);
   const Ranges r = scan_ranges<TB>(p.offsets, E, p.rows, starts, lane);
   const int total = kKind == kWeightGrad ? E * NT * MT : r.total * NT;
   lds_barrier();
@@ -510,6 +525,7 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
   LB b;
   LS sc;
   int ns = 0, left = 0;        // slabs, and what the last one holds (bytes, or rows)
+  bool whole = false;          // ns are the first slabs of more: their last one is whole
 
   // The next task of this workgroup into k, if there is one.
   auto next = [&]() -> bool {
@@ -537,7 +553,7 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
 
   // Slabs are brought in one after the other, into slots 0, 1, ..
   auto issue = [&](bool last, int slot) {
-    const uint32_t at = lds_at + slot * kSlot;
+    const uint32_t at = ring_at + slot * kSlot;
     if (!last) {
       a.full(at, wave);
       b.full(at + TA * kSlabBytes, wave);
@@ -573,9 +589,17 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
       ns = (k.rows + kSlabRows - 1) / kSlabRows;
       left = k.rows - (ns - 1) * kSlabRows;
     }
+    if constexpr (kSplit > 1) {
+      const int from = ns * share / kSplit, to = ns * (share + 1) / kSplit;
+      whole = to < ns;
+      a.base += from * a.step;
+      b.base += from * b.step;
+      if constexpr (kFp4) sc.block += from * LS::kBlocks;
+      ns = to - from;
+    }
 #pragma unroll
     for (int s = 0; s < S; ++s)
-      if (s < ns) issue(s == ns - 1, s);
+      if (s < ns) issue(!whole && s == ns - 1, s);
   };
 
   // Wave (wa, wb) takes MA neighbouring groups of 16 of the A tile and every
@@ -595,7 +619,7 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
   } now, then;
   // Part h of step q of the slab in `slot`.
   auto read = [&](int slot, int q, int h) {
-    const LdsPtr at = (LdsPtr)lds + slot * kSlot;
+    const LdsPtr at = (LdsPtr)ring + slot * kSlot;
 #pragma unroll
     for (int i = 0; i < kPart; ++i) fa[(q * kHalves + h) % 2][i] = ra.get(at, q, h * kPart + i);
     if (h == 0) {
@@ -669,7 +693,7 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
     // slots are constants.
     if (ns > 0) {
       wait_slabs<kPerSlab, S - 1>(kSkipB ? 0 : min(S - 1, ns - 1));
-      lds_barrier();
+      ring_barrier();
       read(0, 0, 0);
       int s = 0;
       for (; s + 2 * S < ns; s += S) {       // every slab brought in here is whole
@@ -677,7 +701,7 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
         for (int i = 0; i < S; ++i) {
           inside(i);
           wait_vm<kPerSlab * (S - 2)>();
-          lds_barrier();
+          ring_barrier();
           issue(false, i);
           read((i + 1) % S, 0, 0);
           multiply(1, kHalves - 1);
@@ -690,8 +714,8 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
             inside(i);
             if (s + i + 1 < ns) {
               wait_slabs<kPerSlab, S - 2>(min(S - 2, ns - 2 - s - i));
-              lds_barrier();
-              if (s + i + S < ns) issue(s + i + S == ns - 1, i);
+              ring_barrier();
+              if (s + i + S < ns) issue(!whole && s + i + S == ns - 1, i);
               read((i + 1) % S, 0, 0);
             }
             multiply(1, kHalves - 1);
@@ -700,6 +724,33 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
       }
     }
     const Task done = k;
+    const int cols = nb;
+    if constexpr (kSplit > 1) {
+      // Wave w takes the sums of every kSplit-th group of B from group w on.
+      floatx4* const sums = reinterpret_cast<floatx4*>(lds);
+      static_assert(MA * MB * 64 * sizeof(floatx4) <= S * kSlot, "the sums take the rings' place");
+      lds_barrier();
+#pragma unroll
+      for (int j = 0; j < MB; ++j)
+#pragma unroll
+        for (int i = 0; i < MA; ++i) sums[((share * MB + j) * MA + i) * 64 + lane] = acc[i][j];
+      lds_barrier();
+#pragma unroll
+      for (int j = 0; j < MB; ++j) {
+        if (j % kSplit != share || j >= cols) continue;
+#pragma unroll
+        for (int i = 0; i < MA; ++i) {
+          floatx4 v = sums[(j * MA + i) * 64 + lane];
+#pragma unroll
+          for (int n = 1; n < kSplit; ++n) {
+            const floatx4 o = sums[((n * MB + j) * MA + i) * 64 + lane];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] += o[c];
+          }
+          acc[i][j] = v;
+        }
+      }
+    }
     have = next();
     if (have) {
       lds_barrier();      // every wave has read the last slab
@@ -708,6 +759,7 @@ __global__ __launch_bounds__(64 * WA * WB) __attribute__((amdgpu_waves_per_eu(2)
 
 #pragma unroll
     for (int j = 0; j < MB; ++j) {
+      if (kSplit > 1 && (j % kSplit != share || j >= cols)) continue;
       const int row = (wb + j * WB) * 16 + (lane & 15);
       const bool row_ok = kKind == kWeightGrad ? done.b0 + row < N : row < done.rows;
       const int64_t at = kKind == kWeightGrad ? (int64_t(done.e) * N + done.b0 + row) * K : (done.row0 + row) * p.ldo;
@@ -855,20 +907,23 @@ int64_t row_tiles(const RaggedArgs& p, int tile) {      // at most
   return int64_t(p.rows) / tile + (p.E < p.rows ? p.E : p.rows);
 }
 
-template <Kind kKind, typename T, int TA, int TB, int WA, int WB, int S>
+template <Kind kKind>
+int64_t task_count(const RaggedArgs& p, int ta, int tb) {
+  const int64_t nt = ((kKind == kForward ? p.N : p.K) + ta - 1) / ta;
+  return nt * (kKind == kWeightGrad ? int64_t(p.E) * ((p.N + tb - 1) / tb) : row_tiles(p, tb));
+}
+
+template <Kind kKind, typename T, int TA, int TB, int WA, int WB, int S, int kSplit = 1>
 hipError_t run(const RaggedArgs& p, hipStream_t stream) {
-  const int64_t OA = kKind == kForward ? p.N : p.K;
-  const int64_t nt = (OA + TA - 1) / TA;
-  const int64_t tasks = kKind == kWeightGrad
-                            ? int64_t(p.E) * nt * ((p.N + TB - 1) / TB)
-                            : row_tiles(p, TB) * nt;
-  constexpr int ring = S * ((TA + TB) * kSlabBytes + ScalesOf<T, TA, TB, WA * WB>::type::kBytes);
+  const int64_t tasks = task_count<kKind>(p, TA, TB);
+  constexpr int ring = kSplit * S * ((TA + TB) * kSlabBytes + ScalesOf<T, TA, TB, WA * WB>::type::kBytes);
   const int lds = ring + (p.E + 1) * 4;
   // As many workgroups as run at once (two waves per SIMD, and by LDS); each
   // takes tasks in turn and loads its next one's first slabs under its stores.
-  const int at_once = kCus * (8 / (WA * WB) < kLdsPerCu / lds ? 8 / (WA * WB) : kLdsPerCu / lds);
-  launch(ragged_gemm<kKind, T, TA, TB, WA, WB, S>, dim3(grid_for((tasks + 7) & ~int64_t(7), at_once)),
-         dim3(64 * WA * WB), lds, stream, p);
+  constexpr int waves = WA * WB * kSplit;
+  const int at_once = kCus * (8 / waves < kLdsPerCu / lds ? 8 / waves : kLdsPerCu / lds);
+  launch(ragged_gemm<kKind, T, TA, TB, WA, WB, S, kSplit>, dim3(grid_for((tasks + 7) & ~int64_t(7), at_once)),
+         dim3(64 * waves), lds, stream, p);
   return hipGetLastError();
 }
 
@@ -889,7 +944,6 @@ hipError_t run_stream(const RaggedArgs& p, hipStream_t stream) {
 // loads of a quarter of the bytes leave more of each line to the cache) only
 // where the tiles would leave CUs idle.
 bool few_rows(const RaggedArgs& p) { return p.rows <= 8 * int64_t(p.E < p.rows ? p.E : p.rows); }
-bool few_tiles(const RaggedArgs& p) { return row_tiles(p, 128) * ((p.N + 127) / 128) < kCus; }
 
 // Columns per workgroup: 16 where 32 would give a CU fewer than four
 // workgroups (bf16, 1 token: 11.8 / 13.2 us; 4 tokens: 39.7 / 37.9).
@@ -899,10 +953,21 @@ hipError_t pick_stream(const RaggedArgs& p, hipStream_t stream) {
   return run_stream<T, 2>(p, stream);
 }
 
+// Tile shapes. 128 x 128 on four waves, two workgroups a CU, is the common one.
+// 64 x 64 with the summed index shared by four waves where those tiles (at
+// most: experts end inside them) fill the CUs about once: 1024 rows of 8
+// experts, N = K = 1024: 13.9 -> 9.2 us; N = 1024, K = 4096: 40.9 -> 19.8; but
+// N = 1536, K = 1024: 14.2 -> 14.9, and a weight gradient of 512 such tiles
+// 7.7 -> 9.8. 256 x 256 for a 16-bit forward product with many rows per expert
+// and tasks for two rounds: 32768 rows, N = 1536, K = 2048, 16 experts 216 ->
+// 195 us, but 128 experts of uneven counts 306 -> 305.
 template <Kind kKind, typename T>
 hipError_t pick(const RaggedArgs& p, hipStream_t stream) {
-  if constexpr (kKind == kForward && !__is_same(T, Fp4) && !__is_same(T, Fp4Odd)) {
-    if (p.rows >= 1024 * int64_t(p.E)) return run<kKind, T, 256, 256, 2, 4, 2>(p, stream);
+  constexpr bool kOdd = __is_same(T, Fp4Odd);
+  if (2 * task_count<kKind>(p, 64, 64) <= 3 * kCus) return run<kKind, T, 64, kOdd ? 32 : 64, 1, 1, 2, 4>(p, stream);
+  if constexpr (kKind == kForward && (__is_same(T, Bf16) || __is_same(T, F16))) {
+    if (p.rows >= 1024 * int64_t(p.E) && task_count<kKind>(p, 256, 256) >= 2 * kCus)
+      return run<kKind, T, 256, 256, 2, 4, 2>(p, stream);
   }
   return run<kKind, T, 128, 128, 2, 2, 2>(p, stream);
 }
@@ -913,7 +978,7 @@ hipError_t launch_ragged_forward(const RaggedArgs& p, int dtype, hipStream_t str
   if (dtype == MOE_DTYPE_MXFP4) {
     const bool words = p.K % 128 == 0 && reinterpret_cast<uintptr_t>(p.a_scale) % 4 == 0 &&
                        reinterpret_cast<uintptr_t>(p.b_scale) % 4 == 0;
-    if (few_rows(p) && few_tiles(p)) return run_stream<Fp4, 1>(p, stream);
+    if (few_rows(p) && task_count<kForward>(p, 128, 128) < kCus) return run_stream<Fp4, 1>(p, stream);
     return words ? pick<kForward, Fp4>(p, stream) : pick<kForward, Fp4Odd>(p, stream);
   }
   if (few_rows(p)) return dtype == MOE_DTYPE_F16 ? pick_stream<F16>(p, stream) : pick_stream<Bf16>(p, stream);

@@ -21,7 +21,20 @@ SHAPES = [
     dict(counts=[65, 31, 32, 33, 1], N=72, K=1032),
     dict(counts=[1100, 700, 5], N=264, K=520, head=3, tail=2),
     dict(counts=[16, 15, 17, 0, 1, 2, 4, 8], N=2048, K=768),
+    # more than 256 experts, and the most
+    dict(counts=[(5 * e) % 4 for e in range(300)], N=72, K=40, head=1, tail=1),
+    dict(counts=[(3 * e) % 2 for e in range(2048)], N=8, K=8),
 ]
+
+# Enough tasks for the larger tiles, in every direction: ends inside tiles,
+# experts without rows, summed extents of one slab, of odd ones and of many.
+LARGE = [
+    dict(counts=[700, 20, 0, 333, 901], N=2056, K=2056, head=5, tail=3),
+    dict(counts=[257, 128, 511, 64], N=2048, K=1544),
+    dict(counts=[1, 1500, 3], N=3096, K=3080, tail=130),
+]
+# Rows per expert for the largest forward tiles (a small K, and one with a tail of eight).
+TALL = [dict(counts=[16500], N=2056, K=64), dict(counts=[5000, 12000], N=2048, K=200, tail=7)]
 
 
 def shape_id(s):

@@ -108,7 +108,10 @@ def product(xq, xs, wq, ws, off, out, pad=0):
 @pytest.mark.parametrize("out", ALL, ids=str)
 @pytest.mark.parametrize("s", [dict(s, K=-(-s["K"] // 32) * 32) for s in R.SHAPES]
                          + [dict(counts=[5, 40], N=40, K=k) for k in (96, 128, 160, 256, 288, 512, 544)]
-                         + [dict(counts=[200, 300, 1], N=264, K=k) for k in (224, 256, 1056)], ids=R.shape_id)
+                         + [dict(counts=[200, 300, 1], N=264, K=k) for k in (224, 256, 1056)]
+                         + [dict(counts=[700, 0, 333, 901], N=2056, K=k, tail=2) for k in (96, 128, 384, 992, 1024)]
+                         + [dict(counts=[1, 2, 0, 1], N=2048, K=k) for k in (32, 480, 512, 1056, 1024)],
+                         ids=R.shape_id)
 def test_product_is_exact(s, out):
     g = torch.Generator().manual_seed(8)
     off, rows = R.offsets_of(s)

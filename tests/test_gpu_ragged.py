@@ -65,6 +65,63 @@ def test_products_are_exact_on_whole_numbers(s, dtype, wide):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("s", R.LARGE, ids=R.shape_id)
+def test_large_tiles_are_exact_on_whole_numbers(s, dtype):
+    g = torch.Generator().manual_seed(12)
+    off, rows = R.offsets_of(s)
+    keep = R.owned(off, rows)
+    E, N, K = len(s["counts"]), s["N"], s["K"]
+    x, dy, w = R.whole(g, rows, K), R.whole(g, rows, N), R.whole(g, E, N, K)
+    announce("ragged large", R.shape_id(s), dtype)
+    xd, dyd = rows_on_gpu(x, dtype, keep, 8), rows_on_gpu(dy, dtype, keep)
+    wd, offd = w.cuda().to(dtype), off.cuda()
+    y, dx = out_rows(rows, N, torch.float32), out_rows(rows, K, dtype, 8)
+    dw = torch.full((E, N, K), float("nan"), dtype=torch.float32, device="cuda")
+    moe.moe_grouped_matmul(xd, wd, offd, y)
+    moe.moe_grouped_matmul_dx(dyd, wd, offd, dx)
+    moe.moe_grouped_matmul_dw(dyd, xd, offd, dw)
+    torch.cuda.synchronize()
+    check_rows(y, R.forward(x, w, off), keep)
+    check_rows(dx, R.input_grad(dy, w, off).to(dtype), keep)
+    assert torch.equal(dw.cpu().double(), R.weight_grad(dy, x, off))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("s", R.TALL, ids=R.shape_id)
+def test_tall_tiles_are_exact_on_whole_numbers(s, dtype):
+    g = torch.Generator().manual_seed(13)
+    off, rows = R.offsets_of(s)
+    keep = R.owned(off, rows)
+    E, N, K = len(s["counts"]), s["N"], s["K"]
+    x, w = R.whole(g, rows, K), R.whole(g, E, N, K)
+    announce("ragged tall", R.shape_id(s), dtype)
+    y = out_rows(rows, N, dtype)
+    moe.moe_grouped_matmul(rows_on_gpu(x, dtype, keep), w.cuda().to(dtype), off.cuda(), y)
+    torch.cuda.synchronize()
+    check_rows(y, R.forward(x, w, off).to(dtype), keep)
+
+
+def test_two_streams_at_once():
+    # Calls share nothing: two of them overlapping on two streams give what each gives alone.
+    g = torch.Generator().manual_seed(14)
+    jobs = []
+    for counts, N, K in (([300, 700], 1032, 520), ([5, 0, 90], 2048, 264)):
+        s = dict(counts=counts, N=N, K=K)
+        off, rows = R.offsets_of(s)
+        x, w = R.whole(g, rows, K), R.whole(g, len(counts), N, K)
+        jobs.append((x.cuda().bfloat16(), w.cuda().bfloat16(), off.cuda(), torch.zeros(rows, N, device="cuda"),
+                     R.forward(x, w, off), torch.cuda.Stream()))
+    announce("ragged two streams")
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for x, w, off, y, _, stream in jobs:
+            moe.moe_grouped_matmul(x, w, off, y, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, _, y, ref, _ in jobs:
+        assert torch.equal(y.double().cpu(), ref)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("out", [torch.float32, None], ids=str)
 @pytest.mark.parametrize("s", [R.SHAPES[i] for i in (3, 5, 8, 9, 10)], ids=R.shape_id)
 def test_products_on_random_values(s, dtype, out):

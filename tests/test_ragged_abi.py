@@ -167,6 +167,8 @@ def test_binding_refuses_bad_tensors_of_the_gradients_and_mxfp4():
         moe.moe_grouped_matmul_dw(bf(4, 16), bf(4, 32), OFF, bf(2, 16, 32))
     with pytest.raises((TypeError, ValueError)):
         moe.moe_grouped_matmul_dw(bf(4, 16), bf(4, 32).half(), OFF, bf(2, 16, 32))
+    with pytest.raises((TypeError, ValueError)):
+        moe.moe_grouped_matmul_dw(bf(4, 16), [1], OFF, bf(2, 16, 32))
     with pytest.raises(ValueError):
         moe.moe_grouped_matmul_mxfp4(torch.zeros(4, 16, dtype=U8), torch.zeros(4, 1, dtype=U8),
                                      torch.zeros(2, 16, 16, dtype=U8), torch.zeros(2, 16, 1, dtype=U8), OFF, bf(4, 16))
@@ -182,6 +184,33 @@ def test_binding_refuses_bad_tensors_of_the_gradients_and_mxfp4():
         moe.moe_mxfp4_dequantize(torch.zeros(4, 16, dtype=U8), torch.zeros(4, 1, dtype=U8), bf(4, 32).half())
     with pytest.raises(ValueError):
         moe.moe_align_offsets(torch.zeros(4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), 2, 1, OFF)
+
+
+def test_calls_run_with_the_tensors_device_current(monkeypatch):
+    # Tensors on another device than the current one: the call is made with
+    # theirs current, on its current stream.
+    seen = []
+
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            seen.append(("enter", self.device.index))
+
+        def __exit__(self, *a):
+            seen.append(("exit", self.device.index))
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 100 + index, raising=False)
+    call = lambda *a: seen.append(a) or 7  # noqa: E731
+    assert B._call_on(torch.device("cuda", 1), None, call, "x") == 7
+    assert seen == [("enter", 1), ("x", 101), ("exit", 1)]
+    seen.clear()
+    assert B._call_on(torch.device("cuda", 0), None, call, "x") == 7
+    assert B._call_on(torch.device("cuda", 0), 55, call, "x") == 7
+    assert seen == [("x", 100), ("x", 55)]
 
 
 def test_reference_quantiser_by_hand():

@@ -25,6 +25,8 @@
 // last one) is read from a zero page instead, in both operands, so that another
 // expert's rows, whatever they hold, cannot reach a sum. What is past the
 // output's extents re-reads the last valid row or chunk and is not stored.
+#include <type_traits>
+
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -402,6 +404,18 @@ struct NoScales {
 // Waits until at most `later` (<= L) slabs' loads of this wave are in flight.
 // Loads return in order among themselves, so other operations in flight only
 // make the wait longer.
+// `stores`: kA or kB stores were issued behind those loads and may stay in
+// flight too, or none is known to (0).
+template <int N, int kA, int kB>
+__device__ __forceinline__ void wait_vm_and(int stores) {
+  if (stores == kA)
+    wait_vm<N + kA>();
+  else if (stores == kB)
+    wait_vm<N + kB>();
+  else
+    wait_vm<N>();
+}
+
 template <int kPerSlab, int L>
 __device__ __forceinline__ void wait_slabs(int later) {
   if constexpr (L == 0) {
@@ -425,7 +439,8 @@ __device__ __forceinline__ uint2 pack16(const floatx4& v, int dtype) {
 // groups change halves between lanes 16 apart, so that a lane holds eight
 // consecutive columns and a store again writes 64 contiguous bytes of a row
 // (stores of 32 bytes a row took up to 1.5 times as long: they go out by line).
-template <int M, typename Get>
+// kAll: rows and columns are known to be valid, and each store is one instruction.
+template <int M, bool kAll, typename Get>
 __device__ __forceinline__ void store_row(void* out, int dtype, int64_t at, int col0, int cols, bool row_ok, int lane,
                                           Get get) {
   const int g = lane >> 4;
@@ -433,7 +448,7 @@ __device__ __forceinline__ void store_row(void* out, int dtype, int64_t at, int 
 #pragma unroll
     for (int i = 0; i < M; ++i) {
       const int col = col0 + i * 16 + 4 * g;
-      if (row_ok && col < cols) *reinterpret_cast<floatx4*>(static_cast<float*>(out) + at + col) = get(i);
+      if (kAll || (row_ok && col < cols)) *reinterpret_cast<floatx4*>(static_cast<float*>(out) + at + col) = get(i);
     }
     return;
   }
@@ -446,13 +461,13 @@ __device__ __forceinline__ void store_row(void* out, int dtype, int64_t at, int 
       const auto lo = __builtin_amdgcn_permlane16_swap(p.x, q.x, false, false);
       const auto hi = __builtin_amdgcn_permlane16_swap(p.y, q.y, false, false);
       const int col = col0 + (i + (g & 1)) * 16 + (g >> 1) * 8;
-      if (row_ok && col < cols) *reinterpret_cast<u32x4*>(o + col) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+      if (kAll || (row_ok && col < cols)) *reinterpret_cast<u32x4*>(o + col) = u32x4{lo[0], hi[0], lo[1], hi[1]};
     }
   } else {
 #pragma unroll
     for (int i = 0; i < M; ++i) {
       const int col = col0 + i * 16 + 4 * g;
-      if (row_ok && col < cols) *reinterpret_cast<uint2*>(o + col) = pack16(get(i), dtype);
+      if (kAll || (row_ok && col < cols)) *reinterpret_cast<uint2*>(o + col) = pack16(get(i), dtype);
     }
   }
 }
@@ -644,6 +659,8 @@ ragged_gemm(const RaggedArgs p) {
     }
   };
 
+  constexpr int kStores16 = MB * MA / 2, kStores32 = MB * MA;   // of a wave, for a tile that is all valid
+  int stores = 0;          // issued behind the loads of this task's first slabs, where their number is known
   bool have = next();
   if (have) begin();
   while (have) {
@@ -692,7 +709,12 @@ ragged_gemm(const RaggedArgs p) {
     // the one S further. Slabs go through the ring in groups of S, so that
     // slots are constants.
     if (ns > 0) {
-      wait_slabs<kPerSlab, S - 1>(kSkipB ? 0 : min(S - 1, ns - 1));
+      // Slab 0, while slab 1 (its A pieces at least) and the stores of the task
+      // before, issued behind them, may be in flight.
+      if (S == 2 && ns > 1)
+        wait_vm_and<kSkipB ? LA::kPer + LS::kPer : kPerSlab, kStores16, kStores32>(stores);
+      else
+        wait_slabs<kPerSlab, S - 1>(kSkipB ? 0 : min(S - 1, ns - 1));
       ring_barrier();
       read(0, 0, 0);
       int s = 0;
@@ -700,7 +722,10 @@ ragged_gemm(const RaggedArgs p) {
 #pragma unroll
         for (int i = 0; i < S; ++i) {
           inside(i);
-          wait_vm<kPerSlab * (S - 2)>();
+          if (S == 2 && i == 0 && s == 0)
+            wait_vm_and<0, kStores16, kStores32>(stores);     // slab 1 is older than the stores
+          else
+            wait_vm<kPerSlab * (S - 2)>();
           ring_barrier();
           issue(false, i);
           read((i + 1) % S, 0, 0);
@@ -713,7 +738,10 @@ ragged_gemm(const RaggedArgs p) {
           if (s + i < ns) {
             inside(i);
             if (s + i + 1 < ns) {
-              wait_slabs<kPerSlab, S - 2>(min(S - 2, ns - 2 - s - i));
+              if (S == 2 && i == 0 && s == 0)
+                wait_vm_and<0, kStores16, kStores32>(stores);
+              else
+                wait_slabs<kPerSlab, S - 2>(min(S - 2, ns - 2 - s - i));
               ring_barrier();
               if (s + i + S < ns) issue(!whole && s + i + S == ns - 1, i);
               read((i + 1) % S, 0, 0);
@@ -757,13 +785,25 @@ ragged_gemm(const RaggedArgs p) {
       begin();            // the next task's loads run under this one's stores
     }
 
+    const bool all = kSplit == 1 && done.a0 + TA <= OA &&
+                     (kKind == kWeightGrad ? done.b0 + TB <= N : done.rows == TB);
+    auto store = [&](auto valid) {
 #pragma unroll
-    for (int j = 0; j < MB; ++j) {
-      if (kSplit > 1 && (j % kSplit != share || j >= cols)) continue;
-      const int row = (wb + j * WB) * 16 + (lane & 15);
-      const bool row_ok = kKind == kWeightGrad ? done.b0 + row < N : row < done.rows;
-      const int64_t at = kKind == kWeightGrad ? (int64_t(done.e) * N + done.b0 + row) * K : (done.row0 + row) * p.ldo;
-      store_row<MA>(p.out, p.out_dtype, at, done.a0 + wa * MA * 16, OA, row_ok, lane, [&](int i) { return acc[i][j]; });
+      for (int j = 0; j < MB; ++j) {
+        if (kSplit > 1 && (j % kSplit != share || j >= cols)) continue;
+        const int row = (wb + j * WB) * 16 + (lane & 15);
+        const bool row_ok = kKind == kWeightGrad ? done.b0 + row < N : row < done.rows;
+        const int64_t at = kKind == kWeightGrad ? (int64_t(done.e) * N + done.b0 + row) * K : (done.row0 + row) * p.ldo;
+        store_row<MA, decltype(valid)::value>(p.out, p.out_dtype, at, done.a0 + wa * MA * 16, OA, row_ok, lane,
+                                              [&](int i) { return acc[i][j]; });
+      }
+    };
+    if (all) {
+      store(std::true_type{});
+      stores = p.out_dtype == MOE_DTYPE_F32 ? kStores32 : kStores16;
+    } else {
+      store(std::false_type{});
+      stores = 0;
     }
   }
 }
@@ -896,7 +936,7 @@ ragged_stream(const RaggedArgs p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] += o[j];
       }
-      store_row<1>(p.out, p.out_dtype, (k.row0 + (lane & 15)) * p.ldo, k.a0 + wave * 16, N, (lane & 15) < k.rows, lane,
+      store_row<1, false>(p.out, p.out_dtype, (k.row0 + (lane & 15)) * p.ldo, k.a0 + wave * 16, N, (lane & 15) < k.rows, lane,
                    [&](int) { return v; });
     }
     lds_barrier();
@@ -959,14 +999,16 @@ hipError_t pick_stream(const RaggedArgs& p, hipStream_t stream) {
 // experts, N = K = 1024: 13.9 -> 9.2 us; N = 1024, K = 4096: 40.9 -> 19.8; but
 // N = 1536, K = 1024: 14.2 -> 14.9, and a weight gradient of 512 such tiles
 // 7.7 -> 9.8. 256 x 256 for a 16-bit forward product with many rows per expert
-// and tasks for two rounds: 32768 rows, N = 1536, K = 2048, 16 experts 216 ->
-// 195 us, but 128 experts of uneven counts 306 -> 305.
+// and tasks for two rounds: 8192 tokens, top-8 of uneven experts, N = 1536, K =
+// 1024: 64 experts 265 -> 241 us, 128 experts 284 -> 268; but 4096 tokens of 128
+// experts, K = 2048: 301 -> 324. The gradients gain or lose 4 % by it and do
+// without.
 template <Kind kKind, typename T>
 hipError_t pick(const RaggedArgs& p, hipStream_t stream) {
   constexpr bool kOdd = __is_same(T, Fp4Odd);
   if (2 * task_count<kKind>(p, 64, 64) <= 3 * kCus) return run<kKind, T, 64, kOdd ? 32 : 64, 1, 1, 2, 4>(p, stream);
   if constexpr (kKind == kForward && (__is_same(T, Bf16) || __is_same(T, F16))) {
-    if (p.rows >= 1024 * int64_t(p.E) && task_count<kKind>(p, 256, 256) >= 2 * kCus)
+    if (p.rows >= 512 * int64_t(p.E) && task_count<kKind>(p, 256, 256) >= 2 * kCus)
       return run<kKind, T, 256, 256, 2, 4, 2>(p, stream);
   }
   return run<kKind, T, 128, 128, 2, 2, 2>(p, stream);

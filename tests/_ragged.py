@@ -32,6 +32,9 @@ LARGE = [
     dict(counts=[700, 20, 0, 333, 901], N=2056, K=2056, head=5, tail=3),
     dict(counts=[257, 128, 511, 64], N=2048, K=1544),
     dict(counts=[1, 1500, 3], N=3096, K=3080, tail=130),
+    # whole tiles only, several to a workgroup
+    dict(counts=[1024, 2048], N=4096, K=192),
+    dict(counts=[1024, 2048], N=192, K=4096),
 ]
 # Rows per expert for the largest forward tiles (a small K, and one with a tail of eight).
 TALL = [dict(counts=[16500], N=2056, K=64), dict(counts=[5000, 12000], N=2048, K=200, tail=7)]

@@ -110,6 +110,7 @@ def product(xq, xs, wq, ws, off, out, pad=0):
                          + [dict(counts=[5, 40], N=40, K=k) for k in (96, 128, 160, 256, 288, 512, 544)]
                          + [dict(counts=[200, 300, 1], N=264, K=k) for k in (224, 256, 1056)]
                          + [dict(counts=[700, 0, 333, 901], N=2056, K=k, tail=2) for k in (96, 128, 384, 992, 1024)]
+                         + [dict(counts=[1024, 2048], N=4096, K=k) for k in (160, 256)]
                          + [dict(counts=[1, 2, 0, 1], N=2048, K=k) for k in (32, 480, 512, 1056, 1024)],
                          ids=R.shape_id)
 def test_product_is_exact(s, out):

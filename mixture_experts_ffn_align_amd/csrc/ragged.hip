@@ -17,7 +17,7 @@
 // bytes of a row (64 16-bit elements, or 256 codes) where the summed index is
 // contiguous in memory ("direct"), or 64 rows where it is the row index
 // ("transposed": W in the input gradient, both operands of the weight
-// gradient). LDS-DMA brings a slab from global memory into a ring of S slots;
+// gradient). LDS-DMA brings a slab from global memory into a ring of two slots;
 // direct tiles are read back 16 bytes a lane, transposed ones with gfx950's
 // transposing LDS read, so neither operand needs a copy in another order.
 //
@@ -51,6 +51,7 @@ enum Kind { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 constexpr int kSteps = 2;                      // matrix steps (32 16-bit elements or 128 codes) per slab
 constexpr int kSlabBytes = 64 * kSteps;        // bytes of a direct row per slab
 constexpr int kSlabRows = 32 * kSteps;         // rows of a transposed operand per slab (16-bit elements)
+constexpr int kSlots = 2;                      // slabs in LDS: one read, one arriving
 constexpr int kCus = 256;
 constexpr int kLdsPerCu = 160 * 1024;
 constexpr int kGroupM = 4;        // row tiles visited together, see find_task
@@ -214,14 +215,11 @@ __device__ __forceinline__ int direct_pos(int row, int c) { return c ^ ((row >> 
 template <int T>   // tile width in 16-bit elements
 __device__ __forceinline__ int trans_unit(int row, int u) {
   constexpr int units = T / 16;
+  static_assert(units == 4 || units >= 8, "rows of 128 bytes, or of 256 and more");
   if constexpr (units >= 8)
     return u ^ ((row & 3) | ((row >> 1) & 4));
-  else if constexpr (units == 4)
-    return u ^ (((row >> 1) & 1) | ((row >> 2) & 2));
-  else if constexpr (units == 2)
-    return u ^ ((row >> 3) & 1);
   else
-    return u;
+    return u ^ (((row >> 1) & 1) | ((row >> 2) & 2));
 }
 
 // One operand's side of the data movement: which bytes this wave brings in.
@@ -231,10 +229,9 @@ __device__ __forceinline__ int trans_unit(int row, int u) {
 template <int T, int NW, bool kTrans, bool kSkip>
 struct Loader {
   static constexpr int kInstr = T * kSlabBytes / 1024;                 // 1 KB pieces per slab
-  static constexpr int kPer = (kInstr + NW - 1) / NW;                  // pieces per wave (some twice where
-                                                                       // they do not divide evenly)
+  static constexpr int kPer = kInstr / NW;                             // pieces per wave
   static constexpr int kPieceRows = 1024 / kSlabBytes;                 // (direct)
-  static_assert(!kSkip || kInstr % NW == 0, "pieces in row order, each once");
+  static_assert(kInstr % NW == 0, "every wave brings in as many pieces");
   const char* base;       // the next slab to bring in
   int64_t step;           // bytes from slab to slab
   uint32_t voff[kPer];    // this lane's offset in each piece
@@ -249,7 +246,7 @@ struct Loader {
     have = uniform(limit - wave * kPieceRows);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int q = ((wave + j * NW) % kInstr) * 64 + lane;   // 16-byte position in the tile
+      const int q = (wave + j * NW) * 64 + lane;   // 16-byte position in the tile
       if constexpr (!kTrans) {
         const int row = q / (kSlabBytes / 16);
         const int c = direct_pos(row, q % (kSlabBytes / 16));   // an XOR is its own inverse
@@ -269,7 +266,7 @@ struct Loader {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       if (kSkip && have <= j * NW * kPieceRows) break;
-      dma16_off(base, voff[j], lds + ((wave + j * NW) % kInstr) * 1024);
+      dma16_off(base, voff[j], lds + (wave + j * NW) * 1024);
     }
     base += step;
   }
@@ -281,7 +278,7 @@ struct Loader {
     for (int j = 0; j < kPer; ++j) {
       const void* src =
           where[j] < left ? static_cast<const void*>(base + voff[j]) : static_cast<const void*>(zero_page);
-      dma16(src, lds + ((wave + j * NW) % kInstr) * 1024);
+      dma16(src, lds + (wave + j * NW) * 1024);
     }
   }
 };
@@ -356,9 +353,10 @@ struct ScaleLoader {
   static constexpr int kBlocks = 4 * kSteps;                           // per row and slab
   static constexpr int kWordsPerRow = kWords ? kSteps : kBlocks;
   static constexpr int kRows = 64 / kWordsPerRow;                      // rows per piece
-  static constexpr int kInstr = (TA + TB + kRows - 1) / kRows;         // pieces per slab
-  static constexpr int kPer = (kInstr + NW - 1) / NW;
+  static constexpr int kInstr = (TA + TB) / kRows;                     // pieces per slab
+  static constexpr int kPer = kInstr / NW;
   static constexpr int kBytes = kInstr * 256;
+  static_assert((TA + TB) % kRows == 0 && kInstr % NW == 0, "every wave brings in as many pieces");
   const uint8_t* src[kPer];
   int block;              // first block of this lane's next word
 
@@ -367,7 +365,7 @@ struct ScaleLoader {
     block = (lane % kWordsPerRow) * (kWords ? 4 : 1);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int row = ((wave + j * NW) % kInstr) * kRows + lane / kWordsPerRow;
+      const int row = (wave + j * NW) * kRows + lane / kWordsPerRow;
       src[j] = row < TA ? a + int64_t(min(row, a_rows - 1)) * per_row : b + int64_t(min(row - TA, b_rows - 1)) * per_row;
     }
   }
@@ -377,7 +375,7 @@ struct ScaleLoader {
     block += kBlocks;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const uint32_t to = lds + ((wave + j * NW) % kInstr) * 256;
+      const uint32_t to = lds + (wave + j * NW) * 256;
       if constexpr (kWords)
         dma4(src[j] + at, to);
       else
@@ -401,31 +399,19 @@ struct NoScales {
   static constexpr int kPer = 0, kBytes = 0;
 };
 
-// Waits until at most `later` (<= L) slabs' loads of this wave are in flight.
-// Loads return in order among themselves, so other operations in flight only
-// make the wait longer.
-// `stores`: kA or kB stores were issued behind those loads and may stay in
-// flight too, or none is known to (0).
+// Waits until at most N loads of this wave, and the stores issued behind them,
+// are in flight: kA or kB stores, or none that are known of (0). Loads and
+// stores of a wave finish in order, so what is issued behind only makes the
+// wait longer.
 template <int N, int kA, int kB>
 __device__ __forceinline__ void wait_vm_and(int stores) {
+  static_assert(N + kA < 64 && N + kB < 64, "vmcnt holds six bits");
   if (stores == kA)
     wait_vm<N + kA>();
   else if (stores == kB)
     wait_vm<N + kB>();
   else
     wait_vm<N>();
-}
-
-template <int kPerSlab, int L>
-__device__ __forceinline__ void wait_slabs(int later) {
-  if constexpr (L == 0) {
-    wait_vm<0>();
-  } else {
-    if (later >= L)
-      wait_vm<kPerSlab * L>();
-    else
-      wait_slabs<kPerSlab, L - 1>(later);
-  }
 }
 
 __device__ __forceinline__ uint2 pack16(const floatx4& v, int dtype) {
@@ -489,7 +475,7 @@ struct ScalesOf<Fp4Odd, TA, TB, NW> {
 // its own and the whole tile's sums, which are added in wave order at the end;
 // for products of few tiles, where a tile's slabs one after the other would be
 // most of the time.
-template <Kind kKind, typename T, int TA, int TB, int WA, int WB, int S, int kSplit>
+template <Kind kKind, typename T, int TA, int TB, int WA, int WB, int kSplit>
 __global__ __launch_bounds__(64 * WA * WB * kSplit) __attribute__((amdgpu_waves_per_eu(2))) void
 ragged_gemm(const RaggedArgs p) {
   static_assert(kSplit == 1 || WA * WB == 1, "waves that share the summed index keep whole tiles");
@@ -499,13 +485,9 @@ ragged_gemm(const RaggedArgs p) {
   constexpr int NW = WA * WB;
   constexpr int MA = TA / WA / 16, MB = TB / WB / 16;
   using LA = Loader<TA, NW, kTransA, false>;
-  // With a ring of two every wait is for all loads, so some may be left out.
-  constexpr bool kSkipB = !kTransB && S == 2 && TB / 8 % NW == 0;
-  using LB = Loader<TB, NW, kTransB, kSkipB>;
+  using LB = Loader<TB, NW, kTransB, !kTransB>;       // no wait counts B's loads, so some may be left out
   using LS = typename ScalesOf<T, TA, TB, NW>::type;
-  constexpr int kPerSlab = LA::kPer + LB::kPer + LS::kPer;
   constexpr int kSlot = (TA + TB) * kSlabBytes + LS::kBytes;    // A tile, B tile, exponents
-  static_assert(kPerSlab * (S - 1) < 64, "vmcnt holds six bits");
   static_assert(kSteps == 2, "fb[q] holds step q of a slab");
   extern __shared__ __align__(16) unsigned char lds[];
 
@@ -513,7 +495,7 @@ ragged_gemm(const RaggedArgs p) {
   const int share = kSplit == 1 ? 0 : uniform(threadIdx.x >> 6);     // of the summed index
   const int wave = kSplit == 1 ? uniform(threadIdx.x >> 6) : 0;
   const int wa = wave % WA, wb = wave / WA;
-  unsigned char* const ring = lds + share * S * kSlot;
+  unsigned char* const ring = lds + share * kSlots * kSlot;
   const uint32_t ring_at = lds_addr(ring);
   // What the waves of a ring wait for before a slot is read or filled again.
   auto ring_barrier = [&]() {
@@ -527,7 +509,7 @@ ragged_gemm(const RaggedArgs p) {
   const int NT = (OA + TA - 1) / TA;
   const int MT = kKind == kWeightGrad ? (N + TB - 1) / TB : 0;
 
-  int* const starts = reinterpret_cast<int*>(lds + kSplit * S * kSlot);
+  int* const starts = reinterpret_cast<int*>(lds + kSplit * kSlots * kSlot);
   const Ranges r = scan_ranges<TB>(p.offsets, E, p.rows, starts, lane);
   const int total = kKind == kWeightGrad ? E * NT * MT : r.total * NT;
   lds_barrier();
@@ -613,7 +595,7 @@ ragged_gemm(const RaggedArgs p) {
       ns = to - from;
     }
 #pragma unroll
-    for (int s = 0; s < S; ++s)
+    for (int s = 0; s < kSlots; ++s)
       if (s < ns) issue(!whole && s == ns - 1, s);
   };
 
@@ -706,45 +688,45 @@ ragged_gemm(const RaggedArgs p) {
     }
     // The next part is read into registers while this one is multiplied.
     // Behind a slab's barrier every wave has read that slab, and its slot takes
-    // the one S further. Slabs go through the ring in groups of S, so that
-    // slots are constants.
+    // the one after the next. Slabs go in pairs, so that slots are constants.
     auto products = [&](auto full) {
-      // Slab 0, while slab 1 (its A pieces at least) and the stores of the task
-      // before, issued behind them, may be in flight.
-      if (S == 2 && ns > 1)
-        wait_vm_and<kSkipB ? LA::kPer + LS::kPer : kPerSlab, kStores16, kStores32>(stores);
+      // Slab 0, while slab 1 (its A pieces and exponents at least) and the
+      // stores of the task before, issued behind them, may be in flight; then
+      // slab 1, while those stores may.
+      if (ns > 1)
+        wait_vm_and<LA::kPer + LS::kPer, kStores16, kStores32>(stores);
       else
-        wait_slabs<kPerSlab, S - 1>(kSkipB ? 0 : min(S - 1, ns - 1));
+        wait_vm<0>();
       ring_barrier();
       read(full, 0, 0, 0);
+      auto wait_next = [&](int s) {
+        if (s == 0)
+          wait_vm_and<0, kStores16, kStores32>(stores);
+        else
+          wait_vm<0>();
+      };
       int s = 0;
-      for (; s + 2 * S < ns; s += S) {       // every slab brought in here is whole
+      for (; s + 2 * kSlots < ns; s += kSlots) {       // every slab brought in here is whole
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
           inside(full, i);
-          if (S == 2 && i == 0 && s == 0)
-            wait_vm_and<0, kStores16, kStores32>(stores);     // slab 1 is older than the stores
-          else
-            wait_vm<kPerSlab * (S - 2)>();
+          wait_next(s + i);
           ring_barrier();
           issue(false, i);
-          read(full, (i + 1) % S, 0, 0);
+          read(full, (i + 1) % kSlots, 0, 0);
           multiply(full, 1, kHalves - 1);
         }
       }
-      for (; s < ns; s += S) {
+      for (; s < ns; s += kSlots) {
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
           if (s + i < ns) {
             inside(full, i);
             if (s + i + 1 < ns) {
-              if (S == 2 && i == 0 && s == 0)
-                wait_vm_and<0, kStores16, kStores32>(stores);
-              else
-                wait_slabs<kPerSlab, S - 2>(min(S - 2, ns - 2 - s - i));
+              wait_next(s + i);
               ring_barrier();
-              if (s + i + S < ns) issue(!whole && s + i + S == ns - 1, i);
-              read(full, (i + 1) % S, 0, 0);
+              if (s + i + kSlots < ns) issue(!whole && s + i + kSlots == ns - 1, i);
+              read(full, (i + 1) % kSlots, 0, 0);
             }
             multiply(full, 1, kHalves - 1);
           }
@@ -762,7 +744,7 @@ ragged_gemm(const RaggedArgs p) {
     if constexpr (kSplit > 1) {
       // Wave w takes the sums of every kSplit-th group of B from group w on.
       floatx4* const sums = reinterpret_cast<floatx4*>(lds);
-      static_assert(MA * MB * 64 * sizeof(floatx4) <= S * kSlot, "the sums take the rings' place");
+      static_assert(MA * MB * 64 * sizeof(floatx4) <= kSlots * kSlot, "the sums take the rings' place");
       lds_barrier();
 #pragma unroll
       for (int j = 0; j < MB; ++j)
@@ -959,16 +941,16 @@ int64_t task_count(const RaggedArgs& p, int ta, int tb) {
   return nt * (kKind == kWeightGrad ? int64_t(p.E) * ((p.N + tb - 1) / tb) : row_tiles(p, tb));
 }
 
-template <Kind kKind, typename T, int TA, int TB, int WA, int WB, int S, int kSplit = 1>
+template <Kind kKind, typename T, int TA, int TB, int WA, int WB, int kSplit = 1>
 hipError_t run(const RaggedArgs& p, hipStream_t stream) {
   const int64_t tasks = task_count<kKind>(p, TA, TB);
-  constexpr int ring = kSplit * S * ((TA + TB) * kSlabBytes + ScalesOf<T, TA, TB, WA * WB>::type::kBytes);
+  constexpr int ring = kSplit * kSlots * ((TA + TB) * kSlabBytes + ScalesOf<T, TA, TB, WA * WB>::type::kBytes);
   const int lds = ring + (p.E + 1) * 4;
   // As many workgroups as run at once (two waves per SIMD, and by LDS); each
   // takes tasks in turn and loads its next one's first slabs under its stores.
   constexpr int waves = WA * WB * kSplit;
   const int at_once = kCus * (8 / waves < kLdsPerCu / lds ? 8 / waves : kLdsPerCu / lds);
-  launch(ragged_gemm<kKind, T, TA, TB, WA, WB, S, kSplit>, dim3(grid_for((tasks + 7) & ~int64_t(7), at_once)),
+  launch(ragged_gemm<kKind, T, TA, TB, WA, WB, kSplit>, dim3(grid_for((tasks + 7) & ~int64_t(7), at_once)),
          dim3(64 * waves), lds, stream, p);
   return hipGetLastError();
 }
@@ -1012,12 +994,12 @@ hipError_t pick_stream(const RaggedArgs& p, hipStream_t stream) {
 template <Kind kKind, typename T>
 hipError_t pick(const RaggedArgs& p, hipStream_t stream) {
   constexpr bool kOdd = __is_same(T, Fp4Odd);
-  if (2 * task_count<kKind>(p, 64, 64) <= 3 * kCus) return run<kKind, T, 64, kOdd ? 32 : 64, 1, 1, 2, 4>(p, stream);
+  if (2 * task_count<kKind>(p, 64, 64) <= 3 * kCus) return run<kKind, T, 64, kOdd ? 32 : 64, 1, 1, 4>(p, stream);
   if constexpr (kKind == kForward && (__is_same(T, Bf16) || __is_same(T, F16))) {
     if (p.rows >= 512 * int64_t(p.E) && task_count<kKind>(p, 256, 256) >= 2 * kCus)
-      return run<kKind, T, 256, 256, 2, 4, 2>(p, stream);
+      return run<kKind, T, 256, 256, 2, 4>(p, stream);
   }
-  return run<kKind, T, 128, 128, 2, 2, 2>(p, stream);
+  return run<kKind, T, 128, 128, 2, 2>(p, stream);
 }
 
 }  // namespace

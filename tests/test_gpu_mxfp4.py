@@ -127,6 +127,24 @@ def test_product_is_exact(s, out):
     assert bool((y[~keep] == SENTINEL).all())
 
 
+def off_by(t, n):
+    """A contiguous GPU copy of `t` that starts n bytes into its buffer."""
+    flat = torch.empty(t.numel() + n, dtype=t.dtype, device="cuda")[n:]
+    return flat.copy_(t.flatten()).view(t.shape)
+
+
+@pytest.mark.parametrize("s", [dict(counts=[1, 2], N=40, K=256), dict(counts=[100, 30], N=72, K=384),
+                               dict(counts=[700, 0, 333, 901], N=2056, K=256)], ids=R.shape_id)
+def test_product_with_exponents_at_odd_addresses(s):
+    g = torch.Generator().manual_seed(15)
+    off, rows = R.offsets_of(s)
+    xq, xs = codes(g, rows, s["K"])
+    wq, ws = codes(g, len(s["counts"]), s["N"], s["K"])
+    announce("mxfp4 odd addresses", R.shape_id(s))
+    y = product(xq, off_by(xs, 1), wq, off_by(ws, 3), off, torch.float32)
+    assert torch.equal(y, R.forward(R.codes_to_values(xq, xs), R.codes_to_values(wq, ws), off))
+
+
 def test_product_of_quantised_values():
     # Whole exponent range of ordinary values; the bound of fp32 sums.
     g = torch.Generator().manual_seed(9)

@@ -239,6 +239,23 @@ def test_infinities_and_nans_stay_in_their_rows(dtype):
     assert torch.equal(torch.nan_to_num(dw, nan=1e30), torch.nan_to_num(R.weight_grad(dy, x, off), nan=1e30))
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("counts", [[3, 2], [100, 61], [900, 800, 700]], ids=str)
+def test_subnormal_inputs(dtype, counts):
+    # The smallest subnormals times whole numbers, scaled so that every product is an ordinary fp32 value.
+    unit = 2.0 ** -24 if dtype == torch.float16 else 2.0 ** -133
+    scale = 1.0 if dtype == torch.float16 else 2.0 ** 60
+    g = torch.Generator().manual_seed(16)
+    off, rows = R.offsets_of(dict(counts=counts))
+    E, N, K = len(counts), 2056, 72
+    x, w = R.whole(g, rows, K) * unit, R.whole(g, E, N, K) * scale
+    announce("ragged subnormals", dtype, counts)
+    y = out_rows(rows, N, torch.float32)
+    moe.moe_grouped_matmul(x.to(dtype).cuda(), w.to(dtype).cuda(), off.cuda(), y)
+    torch.cuda.synchronize()
+    assert torch.equal(y.double().cpu(), R.forward(x, w, off))
+
+
 def test_another_stream_and_replayed_graph():
     s = dict(counts=[65, 0, 200, 7], N=136, K=136)
     off, rows = R.offsets_of(s)

@@ -226,7 +226,7 @@ __device__ __forceinline__ int trans_unit(int row, int u) {
 // kTrans: the tile is [64 rows][T] (the rows are the summed index).
 // kSkip (direct): pieces without a valid row are left out; their LDS then holds
 // whatever was there, which only reaches outputs that are not stored.
-template <int T, int NW, bool kTrans, bool kSkip>
+template <int T, int NW, bool kTrans, bool kSkip, bool kFp4>
 struct Loader {
   static constexpr int kInstr = T * kSlabBytes / 1024;                 // 1 KB pieces per slab
   static constexpr int kPer = kInstr / NW;                             // pieces per wave
@@ -249,7 +249,8 @@ struct Loader {
       const int q = (wave + j * NW) * 64 + lane;   // 16-byte position in the tile
       if constexpr (!kTrans) {
         const int row = q / (kSlabBytes / 16);
-        const int c = direct_pos(row, q % (kSlabBytes / 16));   // an XOR is its own inverse
+        const int x = direct_pos(row, q % (kSlabBytes / 16));   // an XOR is its own inverse
+        const int c = kFp4 ? (x & 3) * 2 + (x >> 2) : x;        // see Reader
         voff[j] = static_cast<uint32_t>(min(row, limit - 1) * ld) + c * 16;
         where[j] = c * 16;
       } else {
@@ -287,9 +288,10 @@ typedef __attribute__((address_space(3))) const unsigned char* LdsPtr;
 
 // This lane's operands of the matrix steps from M groups of 16 tile rows
 // (direct) or columns (transposed) of a tile of width T: group `first` and
-// every kStride-th after it. MXFP4: lane group g of a wave takes blocks 2g and
-// 2g + 1 of a slab, so that its exponents are neighbours.
-template <int T, int M, int kStride, bool kTrans, bool kFp4>
+// every kStride-th after it. In step q lane group g reads the direct tile's
+// position 4q + g, which holds that chunk of a row; for MXFP4 it holds block
+// 2g + q, so that a group's two exponents are neighbours.
+template <int T, int M, int kStride, bool kTrans>
 struct Reader {
   // Offset in the tile: of each step's first group, the others following
   // (direct), or of the first step's groups (transposed).
@@ -300,7 +302,7 @@ struct Reader {
     if constexpr (!kTrans) {
 #pragma unroll
       for (int q = 0; q < kSteps; ++q)
-        at[q] = (first * 16 + i) * kSlabBytes + direct_pos(i, kFp4 ? kSteps * g + q : 4 * q + g) * 16;
+        at[q] = (first * 16 + i) * kSlabBytes + direct_pos(i, 4 * q + g) * 16;
     } else {
       const int row = 8 * g + (i >> 2);
 #pragma unroll
@@ -484,8 +486,8 @@ ragged_gemm(const RaggedArgs p) {
   constexpr bool kTransB = kKind == kWeightGrad;
   constexpr int NW = WA * WB;
   constexpr int MA = TA / WA / 16, MB = TB / WB / 16;
-  using LA = Loader<TA, NW, kTransA, false>;
-  using LB = Loader<TB, NW, kTransB, !kTransB>;       // no wait counts B's loads, so some may be left out
+  using LA = Loader<TA, NW, kTransA, false, kFp4>;
+  using LB = Loader<TB, NW, kTransB, !kTransB, kFp4>;       // no wait counts B's loads, so some may be left out
   using LS = typename ScalesOf<T, TA, TB, NW>::type;
   constexpr int kSlot = (TA + TB) * kSlabBytes + LS::kBytes;    // A tile, B tile, exponents
   static_assert(kSteps == 2, "fb[q] holds step q of a slab");
@@ -605,8 +607,8 @@ ragged_gemm(const RaggedArgs p) {
   // them would not fit the registers beside the sums).
   constexpr int kHalves = MA >= 8 ? 2 : 1;
   constexpr int kPart = MA / kHalves;
-  Reader<TA, MA, 1, kTransA, kFp4> ra;
-  Reader<TB, MB, WB, kTransB, kFp4> rb;
+  Reader<TA, MA, 1, kTransA> ra;
+  Reader<TB, MB, WB, kTransB> rb;
   ra.init(wa * MA, lane);
   rb.init(wb, lane);
   int nb = 0;              // groups of B with a row of the task, for this wave

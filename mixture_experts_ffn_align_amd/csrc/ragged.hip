@@ -473,6 +473,17 @@ struct ScalesOf<Fp4Odd, TA, TB, NW> {
   using type = ScaleLoader<TA, TB, NW, false>;
 };
 
+// A TA x TB tile per task on WA x WB waves. Measured at 4096 tokens, top-8 of
+// 128 experts, N = 1536, K = 2048 (128 x 128 tiles, two workgroups a CU):
+//   forward 299 us (690 TFLOP/s; 1.13 GB of L2 misses at 3.8 TB/s; weights that
+//   sit in cache: 200 us), weight gradient 492 us (805 MB written; a tile has
+//   four slabs, and its start and stores are not hidden: without stores 344 us,
+//   without loads 341), MXFP4 121 us (1.7 PFLOP/s; eight slabs per tile).
+// 8192^3 on one expert: 1301 TFLOP/s (256 x 256 tiles; torch's product 1325).
+// LDS reads are free of bank conflicts and take a sixth of the time; L2 answers
+// in 520 cycles on average. Two slots with the next step's operands held in
+// registers beat more and thinner slots: 64-byte slabs, four deep, 369 us
+// forward (half lines cost the direct operands twice the L2 requests).
 // kSplit > 1: the summed index is shared by kSplit waves, each with a ring of
 // its own and the whole tile's sums, which are added in wave order at the end;
 // for products of few tiles, where a tile's slabs one after the other would be
@@ -804,7 +815,9 @@ ragged_gemm(const RaggedArgs p) {
 // index, so that a single token's products spread over the chip; weights go
 // from memory straight to the matrix instructions' registers, every load of two
 // blocks in flight before the first product. The waves' sums are added in wave
-// order through LDS.
+// order through LDS. One token, eight experts, N = 1536, K = 2048: bf16 11.4 us
+// (50 MB: 4.4 TB/s), MXFP4 6.0 us (13 MB; its start, one round trip to memory
+// and the sums). 21 tokens in bf16: 103 us, 5.4 TB/s.
 constexpr int kStreamWaves = 4;
 constexpr int kBlockBytes = 256;      // of a row per wave and turn: four matrix steps
 

@@ -246,3 +246,25 @@ def test_quantise_and_product_in_a_replayed_graph():
         torch.cuda.synchronize()
         ref = R.forward(R.codes_to_values(*R.quantise(v)), R.codes_to_values(wq, ws), off)
         assert torch.equal(y.double().cpu(), ref)
+
+
+def test_indices_past_32_bits():
+    g = torch.Generator().manual_seed(18)
+    rows, K, N, few = 140000, 32768, 64, 20
+    announce("mxfp4 far rows")
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    xs = R.whole(g, few, K)
+    x[-few:] = xs.to("cuda").to(torch.bfloat16)
+    q, s = gpu_quantise(x)
+    rq, rs = R.quantise(xs)
+    assert torch.equal(q[-few:].cpu(), rq) and torch.equal(s[-few:].cpu(), rs) and not bool(q[:-few].any())
+    moe.moe_mxfp4_dequantize(q, s, x)
+    assert torch.equal(x[-few:].double().cpu(), R.codes_to_values(rq, rs)) and not bool(x[:-few].any())
+    del x
+    wq, ws = codes(g, 1, N, K, lo=127, hi=127)
+    y = torch.empty(rows, N, device="cuda")
+    off = torch.tensor([0, rows], dtype=torch.int32)
+    moe.moe_grouped_matmul_mxfp4(q, s, wq.cuda(), ws.cuda(), off.cuda(), y)
+    # codes of whole numbers up to 4 times multiples of 0.5 up to 6: sums below 2^20 in steps of 0.5
+    assert torch.equal(y[-few:].double().cpu(), R.codes_to_values(rq, rs) @ R.codes_to_values(wq, ws)[0].T)
+    assert bool((y[:-few] == 0).all())

@@ -316,3 +316,54 @@ def test_repeats_are_bitwise_equal():
         got = [t.cpu() for t in (y, dx, dw)]
         first = first or got
         assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
+def test_indices_past_32_bits():
+    # Operands and outputs of more than 2^31 elements: the work is at their far
+    # end, the rest is zero or belongs to experts without rows.
+    g = torch.Generator().manual_seed(17)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+
+    announce("ragged far rows of x")
+    rows, K, N, few = 140000, 16384, 64, 50
+    x = torch.zeros(rows, K, **bf)
+    xs, w = R.whole(g, few, K, top=2), R.whole(g, 1, N, K, top=2)
+    x[-few:] = xs.to("cuda").to(torch.bfloat16)
+    y = torch.empty(rows, N, device="cuda")
+    off = torch.tensor([0, rows], dtype=torch.int32)
+    moe.moe_grouped_matmul(x, w.cuda().to(torch.bfloat16), off.cuda(), y)
+    assert torch.equal(y[-few:].double().cpu(), xs @ w[0].T) and bool((y[:-few] == 0).all())
+    dw = torch.empty(1, N, K, device="cuda")
+    dy = torch.zeros(rows, N, **bf)
+    dys = R.whole(g, few, N, top=2)
+    dy[-few:] = dys.to("cuda").to(torch.bfloat16)
+    moe.moe_grouped_matmul_dw(dy, x, off.cuda(), dw)
+    assert torch.equal(dw[0].double().cpu(), dys.T @ xs)
+    del x, y, dw, dy
+
+    announce("ragged far rows of y")
+    rows, K, N = 300000, 8, 8192
+    x = torch.ones(rows, K, **bf)
+    w = R.whole(g, 1, N, K)
+    y = torch.empty(rows, N, **bf)
+    moe.moe_grouped_matmul(x, w.cuda().to(torch.bfloat16), torch.tensor([0, rows], dtype=torch.int32).cuda(), y)
+    ref = w[0].sum(1).to("cuda").to(torch.bfloat16)
+    assert bool((y[-1000:] == ref).all()) and bool((y[:1000] == ref).all())
+    del x, y
+
+    announce("ragged far experts")
+    E, N, K, few = 70, 8192, 4096, 40
+    w = torch.zeros(E, N, K, **bf)
+    wl = R.whole(g, N, K, top=2)
+    w[-1] = wl.to("cuda").to(torch.bfloat16)
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[-1] = few
+    x, dy = R.whole(g, few, K, top=2), R.whole(g, few, N, top=2)
+    xd, dyd = x.cuda().to(torch.bfloat16), dy.cuda().to(torch.bfloat16)
+    y, dx = torch.empty(few, N, device="cuda"), torch.empty(few, K, device="cuda")
+    moe.moe_grouped_matmul(xd, w, off.cuda(), y)
+    moe.moe_grouped_matmul_dx(dyd, w, off.cuda(), dx)
+    assert torch.equal(y.double().cpu(), x @ wl.T) and torch.equal(dx.double().cpu(), dy @ wl)
+    moe.moe_grouped_matmul_dw(dyd, xd, off.cuda(), w)
+    assert torch.equal(w[-1].double().cpu(), (dy.T @ x).to(torch.bfloat16).double())
+    assert not bool(w[:-1].any())

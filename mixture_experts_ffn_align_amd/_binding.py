@@ -10,6 +10,8 @@ import ctypes
 import os
 import re
 
+import torch
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # The in-tree build; MOE_FFN_LIBRARY names another build of the same sources
 # (the host-sanitizer build of the tests, for one).
@@ -439,14 +441,13 @@ def moe_ffn_resolved_path(desc: moe_ffn_desc) -> int:
 # checks are one expression per tensor; which rule failed is worked out only
 # then.
 
-_dtype_codes = {}
+_dtype_codes = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
 
 
 def _dtype_code(name, t, allowed) -> int:
     """moe_dtype of tensor ``t``; TypeError unless it is one of ``allowed``."""
     if not _dtype_codes:
-        import torch
-        _dtype_codes.update({torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16,
+            _dtype_codes.update({torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16,
                              torch.float16: MOE_DTYPE_F16})
     code = _dtype_codes.get(getattr(t, "dtype", None))
     if code not in allowed:
@@ -483,7 +484,6 @@ def _expect_rows(name, t, shape, device=None):
 def _call_on(device, stream, fn, *args) -> int:
     """fn(*args, stream) with ``device`` current; ``stream`` None is the
     device's current stream."""
-    import torch
     index = device.index
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else getattr(stream, "cuda_stream", stream)
     if index == torch.cuda.current_device():
@@ -510,7 +510,6 @@ def moe_grouped_matmul(x, w, offsets, y, stream=None, check: bool = True) -> int
     x [rows, K] and w [E, N, K] bf16 or fp16, offsets [E + 1] int32 (expert e owns
     rows offsets[e] .. offsets[e + 1] - 1), y [rows, N] of x's dtype or fp32. x and
     y may have a row stride. Rows no expert owns are left as they were."""
-    import torch
     E, N, K = _expect_3d("w", w)
     dt = _dtype_code("x", x, _GMM_TYPES)
     out = _dtype_code("y", y, (dt, MOE_DTYPE_F32))
@@ -533,7 +532,6 @@ def moe_grouped_matmul_dx(dy, w, offsets, dx, stream=None, check: bool = True) -
 
     dy [rows, N] and w [E, N, K] bf16 or fp16, offsets as there, dx [rows, K] of
     dy's dtype or fp32."""
-    import torch
     E, N, K = _expect_3d("w", w)
     dt = _dtype_code("dy", dy, _GMM_TYPES)
     out = _dtype_code("dx", dx, (dt, MOE_DTYPE_F32))
@@ -557,7 +555,6 @@ def moe_grouped_matmul_dw(dy, x, offsets, dw, stream=None, check: bool = True) -
 
     dy [rows, N] and x [rows, K] bf16 or fp16, offsets as there, dw [E, N, K] of
     their dtype or fp32."""
-    import torch
     E, N, K = _expect_3d("dw", dw)
     dt = _dtype_code("dy", dy, _GMM_TYPES)
     out = _dtype_code("dw", dw, (dt, MOE_DTYPE_F32))
@@ -581,7 +578,6 @@ def moe_grouped_matmul_mxfp4(xq, x_scale, wq, w_scale, offsets, y, stream=None, 
 
     xq [rows, K/2], x_scale [rows, K/32], wq [E, N, K/2], w_scale [E, N, K/32] uint8,
     offsets as there, y [rows, N] bf16, fp16 or fp32."""
-    import torch
     E, N, half = _expect_3d("wq", wq)
     K = 2 * half
     out = _dtype_code("y", y, _ALL_TYPES)
@@ -607,7 +603,6 @@ def moe_grouped_matmul_mxfp4(xq, x_scale, wq, w_scale, offsets, y, stream=None, 
 def _mxfp4_rows(name, t, q, scale):
     """(rows, K, row stride) of the values ``t`` [.., K] beside codes ``q`` [.., K/2]
     and exponents ``scale`` [.., K/32]."""
-    import torch
     if t.dim() < 2:
         raise ValueError(f"{name}: expected [.., K], got shape {tuple(t.shape)}")
     *lead, K = t.shape
@@ -653,7 +648,6 @@ def moe_align_offsets(expert_block_ids, num_padded, E: int, b: int, offsets, str
                       check: bool = True) -> int:
     """Row offsets [E + 1] int32 of moe_align's blocks, as moe_grouped_matmul takes
     them; with b == 1 expert e's routes are sorted_route_ids[offsets[e]:offsets[e + 1]]."""
-    import torch
     if not hasattr(expert_block_ids, "data_ptr"):
         raise TypeError(f"expert_block_ids: expected a torch.Tensor, got {type(expert_block_ids).__name__}")
     n = expert_block_ids.numel()

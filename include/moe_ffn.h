@@ -318,7 +318,7 @@ typedef enum {
  * cols, a multiple of 8, at most 2^22) and 16-byte aligned; w and dw are
  * contiguous and 16-byte aligned. Outputs may not overlap inputs. */
 typedef struct {
-  int32_t rows;       /* rows of the row operands (>= 0) */
+  int32_t rows;       /* rows of the row operands (0..2^31 - 256) */
   int32_t E;          /* experts (1..2048) */
   int32_t N;          /* output features: rows of an expert's weights; a multiple of 8, at most 2^20 */
   int32_t K;          /* input features; a multiple of 8 (MXFP4: of 32), at most 2^20 */

@@ -10,6 +10,7 @@ namespace {
 
 constexpr int32_t kMaxExperts = 2048;
 constexpr int32_t kMaxDim = 1 << 20;          // N, K
+constexpr int32_t kMaxRows = INT32_MAX - 255; // a tile's last row, and the rounding up of a row count to tiles, stay int32
 constexpr int64_t kMaxStride = 1 << 22;       // row strides: a tile's 256 rows stay within 32-bit byte offsets
 constexpr int64_t kMaxTasks = int64_t(1) << 30;
 constexpr int64_t kMaxElements = int64_t(1) << 40;   // MXFP4 calls
@@ -26,7 +27,7 @@ moe_status check_shape(const moe_grouped_matmul_desc* d, int32_t unit) {
   if (d->rows < 0 || d->E < 1 || d->N < 1 || d->K < 1) return MOE_ERR_INVALID_ARG;
   if (d->N % 8 != 0 || d->K % unit != 0) return MOE_ERR_INVALID_ARG;
   if (!is_dtype(d->out_dtype)) return MOE_ERR_INVALID_ARG;
-  if (d->E > kMaxExperts || d->N > kMaxDim || d->K > kMaxDim) return MOE_ERR_UNSUPPORTED;
+  if (d->rows > kMaxRows || d->E > kMaxExperts || d->N > kMaxDim || d->K > kMaxDim) return MOE_ERR_UNSUPPORTED;
   // Tasks of the smallest tiles (16 x 16) in every direction.
   const int64_t nt = (d->N + 15) / 16, kt = (d->K + 15) / 16;
   const int64_t mt = d->rows / 16 + int64_t(d->E);

@@ -492,6 +492,23 @@ def _call_on(device, stream, fn, *args) -> int:
         return fn(*args, raw)
 
 
+_I32_MAX = 2 ** 31 - 1
+
+
+def _expect_i32(**sizes):
+    """ValueError for the first size that does not fit the C ABI's int32 (ctypes
+    drops its upper bits instead of failing)."""
+    for name, v in sizes.items():
+        if not -_I32_MAX <= v <= _I32_MAX:
+            raise ValueError(f"{name}: {v} does not fit 32 bits")
+
+
+def _gmm_desc(rows, E, N, K, dtype, out_dtype):
+    if rows > _I32_MAX or E > _I32_MAX or N > _I32_MAX or K > _I32_MAX:
+        _expect_i32(rows=rows, E=E, N=N, K=K)
+    return moe_grouped_matmul_desc(rows, E, N, K, dtype, out_dtype)
+
+
 _GMM_TYPES = (MOE_DTYPE_BF16, MOE_DTYPE_F16)
 _ALL_TYPES = (MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16)
 
@@ -519,7 +536,7 @@ def moe_grouped_matmul(x, w, offsets, y, stream=None, check: bool = True) -> int
     _expect_like("w", w, x.dtype, (E, N, K), dev)
     _expect_like("offsets", offsets, torch.int32, (E + 1,), dev)
     ldy = _expect_rows("y", y, (rows, N), dev)
-    d = moe_grouped_matmul_desc(rows, E, N, K, dt, out)
+    d = _gmm_desc(rows, E, N, K, dt, out)
     st = _call_on(dev, stream, lib().moe_grouped_matmul, ctypes.byref(d), x.data_ptr(), ldx, w.data_ptr(),
                   offsets.data_ptr(), y.data_ptr(), ldy)
     if check:
@@ -541,7 +558,7 @@ def moe_grouped_matmul_dx(dy, w, offsets, dx, stream=None, check: bool = True) -
     _expect_like("w", w, dy.dtype, (E, N, K), dev)
     _expect_like("offsets", offsets, torch.int32, (E + 1,), dev)
     lddx = _expect_rows("dx", dx, (rows, K), dev)
-    d = moe_grouped_matmul_desc(rows, E, N, K, dt, out)
+    d = _gmm_desc(rows, E, N, K, dt, out)
     st = _call_on(dev, stream, lib().moe_grouped_matmul_dx, ctypes.byref(d), dy.data_ptr(), lddy, w.data_ptr(),
                   offsets.data_ptr(), dx.data_ptr(), lddx)
     if check:
@@ -565,7 +582,7 @@ def moe_grouped_matmul_dw(dy, x, offsets, dw, stream=None, check: bool = True) -
     ldx = _expect_rows("x", x, (rows, K), dev)
     _expect_like("offsets", offsets, torch.int32, (E + 1,), dev)
     _expect_like("dw", dw, dw.dtype, (E, N, K), dev)
-    d = moe_grouped_matmul_desc(rows, E, N, K, dt, out)
+    d = _gmm_desc(rows, E, N, K, dt, out)
     st = _call_on(dev, stream, lib().moe_grouped_matmul_dw, ctypes.byref(d), dy.data_ptr(), lddy, x.data_ptr(),
                   ldx, offsets.data_ptr(), dw.data_ptr())
     if check:
@@ -592,7 +609,7 @@ def moe_grouped_matmul_mxfp4(xq, x_scale, wq, w_scale, offsets, y, stream=None, 
     _expect_like("w_scale", w_scale, torch.uint8, (E, N, K // 32), dev)
     _expect_like("offsets", offsets, torch.int32, (E + 1,), dev)
     ldy = _expect_rows("y", y, (rows, N), dev)
-    d = moe_grouped_matmul_desc(rows, E, N, K, MOE_DTYPE_MXFP4, out)
+    d = _gmm_desc(rows, E, N, K, MOE_DTYPE_MXFP4, out)
     st = _call_on(dev, stream, lib().moe_grouped_matmul_mxfp4, ctypes.byref(d), xq.data_ptr(), x_scale.data_ptr(),
                   wq.data_ptr(), w_scale.data_ptr(), offsets.data_ptr(), y.data_ptr(), ldy)
     if check:
@@ -614,6 +631,8 @@ def _mxfp4_rows(name, t, q, scale):
         ld, rows = K, 1
         for n in lead:
             rows *= n
+    if K > _I32_MAX:
+        _expect_i32(K=K)
     dev = t.device
     _expect_like("q", q, torch.uint8, (*lead, K // 2), dev)
     _expect_like("scale", scale, torch.uint8, (*lead, K // 32), dev)
@@ -657,6 +676,7 @@ def moe_align_offsets(expert_block_ids, num_padded, E: int, b: int, offsets, str
     _expect_like("expert_block_ids", expert_block_ids, torch.int32, (n,), dev)
     _expect_like("num_padded", num_padded, torch.int32, (1,), dev)
     _expect_like("offsets", offsets, torch.int32, (E + 1,), dev)
+    _expect_i32(E=E, b=b)
     st = _call_on(dev, stream, lib().moe_align_offsets, expert_block_ids.data_ptr(), num_padded.data_ptr(), n, E, b,
                   offsets.data_ptr())
     if check:

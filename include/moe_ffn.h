@@ -381,7 +381,9 @@ MOE_API moe_status moe_mxfp4_dequantize(int32_t dtype, const void* q, const uint
  * offsets[e] = b * (blocks of experts below e), int32 [E + 1], from
  * moe_align's expert_block_ids (`blocks` entries: capacity / b), num_padded
  * and b. With b == 1 the aligned rows have no padding, and expert e's are
- * sorted_route_ids[offsets[e]] .. [offsets[e + 1] - 1].
+ * sorted_route_ids[offsets[e]] .. [offsets[e + 1] - 1]; entries from offsets[E]
+ * on hold the sentinel M*k, which is no route (and M*k / k no token). With b > 1
+ * an expert's rows end with padding, which the products treat as rows of it.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (E > 2048, blocks * b above
  * INT32_MAX), MOE_ERR_HIP. */
 MOE_API moe_status moe_align_offsets(const int32_t* expert_block_ids, const int32_t* num_padded, size_t blocks,

@@ -85,3 +85,22 @@ def test_binding_refuses_sizes_past_32_bits(calls, name, call):
     with pytest.raises(ValueError, match=f"^{name}: "):
         call(PAST)
     assert len(calls) == 1
+
+
+@pytest.mark.gpu
+def test_the_most_rows_of_one_expert():
+    # 2^31 - 256 rows of eight elements (34 GB), all of one expert: forward and input gradient.
+    rows, N, K = INT32_MAX - 255, 8, 8
+    print("[gpu-case] ragged most rows", flush=True)
+    w = torch.arange(N * K, dtype=torch.float32).view(1, N, K) % 7
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    x = torch.ones(rows, K, dtype=torch.bfloat16, device="cuda")
+    x[-300:] = 2.0
+    y = torch.zeros(rows, N, dtype=torch.bfloat16, device="cuda")
+    for call, ref in ((moe.moe_grouped_matmul, w[0].sum(1)), (moe.moe_grouped_matmul_dx, w[0].sum(0))):
+        y.zero_()
+        call(x, w.cuda().bfloat16(), off, y)
+        ref = ref.cuda().bfloat16()
+        for r in range(0, rows, 1 << 28):
+            assert bool((y[r:min(rows - 300, r + (1 << 28))] == ref).all())
+        assert bool((y[-300:] == 2 * ref).all())

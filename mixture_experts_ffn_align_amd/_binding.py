@@ -446,9 +446,6 @@ _dtype_codes = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, to
 
 def _dtype_code(name, t, allowed) -> int:
     """moe_dtype of tensor ``t``; TypeError unless it is one of ``allowed``."""
-    if not _dtype_codes:
-            _dtype_codes.update({torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16,
-                             torch.float16: MOE_DTYPE_F16})
     code = _dtype_codes.get(getattr(t, "dtype", None))
     if code not in allowed:
         if not hasattr(t, "data_ptr"):

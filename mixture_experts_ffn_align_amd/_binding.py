@@ -673,7 +673,8 @@ def moe_align_offsets(expert_block_ids, num_padded, E: int, b: int, offsets, str
     _expect_like("expert_block_ids", expert_block_ids, torch.int32, (n,), dev)
     _expect_like("num_padded", num_padded, torch.int32, (1,), dev)
     _expect_like("offsets", offsets, torch.int32, (E + 1,), dev)
-    _expect_i32(E=E, b=b)
+    if E > _I32_MAX or not -_I32_MAX <= b <= _I32_MAX:
+        _expect_i32(E=E, b=b)
     st = _call_on(dev, stream, lib().moe_align_offsets, expert_block_ids.data_ptr(), num_padded.data_ptr(), n, E, b,
                   offsets.data_ptr())
     if check:

@@ -86,7 +86,7 @@ __global__ __launch_bounds__(kThreads) void mxfp4_quantize(const void* __restric
 }
 
 // A lane decodes eight codes; 196608 x 2048 to bf16 191 us, 5.3 TB/s. Every value is exact in bf16 and fp32 (but
-// 6 * 2^126 and above, which is infinite; the quantiser above does not make them).
+// those from 2^128 on, which are infinite; the quantiser above does not make them).
 template <int kDtype>
 __global__ __launch_bounds__(kThreads) void mxfp4_dequantize(const uint32_t* __restrict__ q,
                                                              const uint8_t* __restrict__ scale, int64_t rows,

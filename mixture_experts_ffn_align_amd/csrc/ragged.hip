@@ -475,15 +475,19 @@ struct ScalesOf<Fp4Odd, TA, TB, NW> {
 
 // A TA x TB tile per task on WA x WB waves. Measured at 4096 tokens, top-8 of
 // 128 experts, N = 1536, K = 2048 (128 x 128 tiles, two workgroups a CU):
-//   forward 299 us (690 TFLOP/s; 1.13 GB of L2 misses at 3.8 TB/s; weights that
-//   sit in cache: 200 us), weight gradient 492 us (805 MB written; a tile has
-//   four slabs, and its start and stores are not hidden: without stores 344 us,
-//   without loads 341), MXFP4 121 us (1.7 PFLOP/s; eight slabs per tile).
-// 8192^3 on one expert: 1301 TFLOP/s (256 x 256 tiles; torch's product 1325).
-// LDS reads are free of bank conflicts and take a sixth of the time; L2 answers
-// in 520 cycles on average. Two slots with the next step's operands held in
-// registers beat more and thinner slots: 64-byte slabs, four deep, 369 us
-// forward (half lines cost the direct operands twice the L2 requests).
+//   forward 298 us (693 TFLOP/s; 1.2 GB of L2 misses at 4.2 TB/s; without loads
+//   207 us, without stores 281), at 2.1 GHz; back to back the clock falls as far
+//   as 1.7 GHz and the time rises to 330 us;
+//   weight gradient 464 to 550 us by where the busiest experts come in the order
+//   of tasks (805 MB written; a tile has four slabs, and its start and stores are
+//   not hidden: without stores 299 to 344 us, without loads 288 to 320);
+//   MXFP4 121 us (1.7 PFLOP/s; eight slabs per tile; without stores 120 us where
+//   the whole takes 140, without loads 93 to 107).
+// 8192^3 on one expert: 1210 TFLOP/s (256 x 256 tiles), where torch's product
+// reaches 1382. Of 29 M cycles of LDS reads 8192 are bank conflicts; L2
+// answers in 510 cycles on average. Two slots with the next step's operands held
+// in registers beat more and thinner slots: 64-byte slabs, four deep, 369 us
+// against 306 forward (half lines cost the direct operands twice the L2 requests).
 // kSplit > 1: the summed index is shared by kSplit waves, each with a ring of
 // its own and the whole tile's sums, which are added in wave order at the end;
 // for products of few tiles, where a tile's slabs one after the other would be
@@ -815,9 +819,9 @@ ragged_gemm(const RaggedArgs p) {
 // index, so that a single token's products spread over the chip; weights go
 // from memory straight to the matrix instructions' registers, every load of two
 // blocks in flight before the first product. The waves' sums are added in wave
-// order through LDS. One token, eight experts, N = 1536, K = 2048: bf16 11.4 us
-// (50 MB: 4.4 TB/s), MXFP4 6.0 us (13 MB; its start, one round trip to memory
-// and the sums). 21 tokens in bf16: 103 us, 5.4 TB/s.
+// order through LDS. One token, eight experts, N = 1536, K = 2048: bf16 10.7 us
+// (50 MB: 4.7 TB/s), MXFP4 6.0 us (13 MB; its start, one round trip to memory
+// and the sums). 21 tokens in bf16: 104 us, 5.7 TB/s.
 constexpr int kStreamWaves = 4;
 constexpr int kBlockBytes = 256;      // of a row per wave and turn: four matrix steps
 
@@ -980,16 +984,18 @@ hipError_t run_stream(const RaggedArgs& p, hipStream_t stream) {
 
 // Which kernel: ragged_stream fills the chip with few rows, ragged_gemm reads
 // weights in whole 128-byte lines and shares them between the rows of a tile.
-// Measured at N = 1536, K = 2048, 128 experts, top-8 (us, stream / tiles):
-//   bf16, tokens 1: 11.8 / 20.0, 4: 37.9 / 42.2, 21: 103 / 124, 128: 143 / 150, 256: 197 / 163;
-//   MXFP4, tokens 1: 6.6 / 10.5, 4: 16.4 / 14.1, 21: 51.4 / 38.4.
+// Measured at N = 1536, K = 2048, 128 experts, top-8 (us per call, stream / tiles):
+//   bf16, tokens 1: 11.9 / 12.4, 4: 38.0 / 41.9, 21: 104 / 124, 64: 142 / 158, 128: 155 / 171, 256: 210 / 174;
+//   MXFP4, tokens 1: 9.2 / 9.1, 4: 16.6 / 14.3, 21: 51.5 / 37.7.
 // So 16-bit operands stream up to eight rows per expert, MXFP4 (a stream's
 // loads of a quarter of the bytes leave more of each line to the cache) only
-// where the tiles would leave CUs idle.
+// where the tiles would leave CUs idle. The host knows the average alone: 1024
+// rows that all belong to one of the 128 experts stream too, sixteen rows to a
+// task, in 78 us where tiles take 25.
 bool few_rows(const RaggedArgs& p) { return p.rows <= 8 * int64_t(p.E < p.rows ? p.E : p.rows); }
 
 // Columns per workgroup: 16 where 32 would give a CU fewer than four
-// workgroups (bf16, 1 token: 11.8 / 13.2 us; 4 tokens: 39.7 / 37.9).
+// workgroups (bf16, 1 token: 11.6 / 12.9 us; 4 tokens: 38.7 / 37.7).
 template <typename T>
 hipError_t pick_stream(const RaggedArgs& p, hipStream_t stream) {
   if (row_tiles(p, 16) * ((p.N + 31) / 32) < 4 * kCus) return run_stream<T, 1>(p, stream);
@@ -999,13 +1005,14 @@ hipError_t pick_stream(const RaggedArgs& p, hipStream_t stream) {
 // Tile shapes. 128 x 128 on four waves, two workgroups a CU, is the common one.
 // 64 x 64 with the summed index shared by four waves where those tiles (at
 // most: experts end inside them) fill the CUs about once: 1024 rows of 8
-// experts, N = K = 1024: 13.9 -> 9.2 us; N = 1024, K = 4096: 40.9 -> 19.8; but
-// N = 1536, K = 1024: 14.2 -> 14.9, and a weight gradient of 512 such tiles
-// 7.7 -> 9.8. 256 x 256 for a 16-bit forward product with many rows per expert
+// experts, N = K = 1024: 14.7 -> 10.4 us; N = 1024, K = 4096: 61.6 -> 26.1; but
+// N = 1536, K = 1024: 15.4 -> 16.7, and a weight gradient of 512 such tiles
+// 8.2 -> 9.5. 256 x 256 for a 16-bit forward product with many rows per expert
 // and tasks for two rounds: 8192 tokens, top-8 of uneven experts, N = 1536, K =
-// 1024: 64 experts 265 -> 241 us, 128 experts 284 -> 268; but 4096 tokens of 128
-// experts, K = 2048: 301 -> 324. The gradients gain or lose 4 % by it and do
-// without.
+// 1024: 64 experts 302 -> 278 us, 128 experts 320 -> 318; 32768 rows shared
+// evenly by 16 experts, K = 2048: 261 -> 228. With 256 rows per expert nothing
+// is sure: 4096 tokens of 128 experts, K = 2048: 352 -> 346 on one card, 301 ->
+// 324 on another. The gradients gain or lose 4 % by it and do without.
 template <Kind kKind, typename T>
 hipError_t pick(const RaggedArgs& p, hipStream_t stream) {
   constexpr bool kOdd = __is_same(T, Fp4Odd);

@@ -523,7 +523,8 @@ def moe_grouped_matmul(x, w, offsets, y, stream=None, check: bool = True) -> int
 
     x [rows, K] and w [E, N, K] bf16 or fp16, offsets [E + 1] int32 (expert e owns
     rows offsets[e] .. offsets[e + 1] - 1), y [rows, N] of x's dtype or fp32. x and
-    y may have a row stride. Rows no expert owns are left as they were."""
+    y may have a row stride. Rows no expert owns are left as they were. Autograd
+    does not see the call: its gradients are moe_grouped_matmul_dx and _dw."""
     E, N, K = _expect_3d("w", w)
     dt = _dtype_code("x", x, _GMM_TYPES)
     out = _dtype_code("y", y, (dt, MOE_DTYPE_F32))

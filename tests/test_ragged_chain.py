@@ -72,3 +72,61 @@ def test_chain_of_a_shard(M, E, shard, base):
     assert torch.equal(y[:n].double().cpu(), R.forward(xr, w, off)) and bool((y[n:] == 7.5).all())
     assert torch.equal(dx[:n].double().cpu(), R.input_grad(dy[:n], w, off)) and bool((dx[n:] == 7.5).all())
     assert torch.equal(dw.double().cpu(), R.weight_grad(dy[:n], xr, off))
+
+
+class Product(torch.autograd.Function):
+    """What a training step writes around the raw calls."""
+
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        y = torch.zeros(x.shape[0], w.shape[1], dtype=x.dtype, device=x.device)
+        moe.moe_grouped_matmul(x, w, offsets, y)
+        ctx.save_for_backward(x, w, offsets)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, offsets = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx, dw = torch.zeros_like(x), torch.empty_like(w)
+        moe.moe_grouped_matmul_dx(dy, w, offsets, dx)
+        moe.moe_grouped_matmul_dw(dy, x, offsets, dw)
+        return dx, dw, None
+
+
+@pytest.mark.gpu
+def test_training_step_of_an_expert_layer():
+    # Two products with a threshold between them, gathered from and summed back into tokens, some routes
+    # without an expert. Every value and gradient is a whole number up to 256, exact in bf16.
+    M, k, E, H, I = 40, 2, 5, 24, 16
+    print("[gpu-case] ragged training step", flush=True)
+    g = torch.Generator().manual_seed(31)
+    ids = torch.stack([torch.randperm(E + 1, generator=g)[:k] for _ in range(M)]).to(torch.int32)   # E is no expert
+
+    def sparse(*shape):
+        return (torch.randint(-1, 2, shape, generator=g) * (torch.rand(*shape, generator=g) < 0.3)).double()
+
+    x, w1, w2, dy = sparse(M, H), sparse(E, I, H), sparse(E, H, I), sparse(M, H)
+
+    i32 = dict(dtype=torch.int32, device="cuda")
+    routes, blocks, num_padded, offsets = (torch.empty(n, **i32) for n in (M * k, M * k, 1, E + 1))
+    moe.moe_align(ids.cuda(), E, 1, routes, blocks, num_padded)
+    moe.moe_align_offsets(blocks, num_padded, E, 1, offsets)
+    leaves = [t.cuda().bfloat16().requires_grad_() for t in (x, w1, w2)]
+    token = (routes // k).clamp(max=M - 1).long()
+    live = (routes < M * k).unsqueeze(1)
+    a = Product.apply(leaves[0][token], leaves[1], offsets).relu()
+    y = torch.zeros(M, H, device="cuda").index_add(0, token, Product.apply(a, leaves[2], offsets).float() * live)
+    y.backward(dy.cuda().float())
+
+    ref = [t.clone().requires_grad_() for t in (x, w1, w2)]
+    out = torch.zeros(M, H, dtype=torch.float64)
+    for r, e in enumerate(ids.flatten().tolist()):
+        if e < E:
+            out = out.index_add(0, torch.tensor([r // k]), (ref[2][e] @ (ref[1][e] @ ref[0][r // k]).relu()).unsqueeze(0))
+    out.backward(dy)
+    largest = max(float(t.detach().abs().max()) for t in (out, *(r.grad for r in ref)))
+    assert 4 < largest <= 256                # what bf16 holds exactly
+    assert torch.equal(y.detach().double().cpu(), out.detach())
+    for t, r in zip(leaves, ref):
+        assert torch.equal(t.grad.double().cpu(), r.grad)

@@ -389,6 +389,133 @@ MOE_API moe_status moe_mxfp4_dequantize(int32_t dtype, const void* q, const uint
 MOE_API moe_status moe_align_offsets(const int32_t* expert_block_ids, const int32_t* num_padded, size_t blocks,
                                      int32_t E, int32_t b, int32_t* offsets, hipStream_t stream);
 
+/* Score of an expert as a function of its logit. */
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0,   /* softmax over all E logits */
+  MOE_SCORE_SIGMOID = 1    /* sigmoid of each logit */
+} moe_score;
+
+/* Routing of M tokens to k of E experts: what topk_ids and topk_w of the layer
+ * above hold (its w[t,j]; the pages take them as given). */
+typedef struct {
+  int32_t M;            /* tokens (0..2^31 - 256) */
+  int32_t E;            /* experts (1..2048) */
+  int32_t k;            /* routes per token (1..min(E, 64)) */
+  int32_t dtype;        /* moe_dtype of the logits: MOE_DTYPE_F32, _BF16 or _F16 */
+  int32_t score;        /* moe_score */
+  int32_t renormalize;  /* nonzero: weights are divided by the sum of the chosen scores */
+  float scale;          /* factor of the weights */
+  int32_t groups;       /* equal runs of consecutive experts (1..64, divides E); 1: no groups */
+  int32_t topk_groups;  /* groups a token may choose from (1..groups); they hold at least k experts */
+  int32_t group_top;    /* 1 or 2: a group ranks by the sum of its 1 or 2 largest choice values */
+} moe_route_desc;
+
+/* For each token: scores s_e of the logits, choice values c_e = s_e + bias_e
+ * (without a bias the order of the logits, which is the order of the scores), the
+ * topk_groups groups that rank highest, and of their experts the k with the
+ * largest choice values, in descending order. Ties go to the lowest index, of
+ * groups too. Weight of a chosen expert: scale * s_e, divided by the sum of the
+ * chosen scores with `renormalize`; the bias has no part in it.
+ *   logits    [M][E], stride ld elements (>= E, at most 2^22), no alignment
+ *             beyond its elements'
+ *   bias      fp32 [E] or NULL
+ *   topk_ids  int32 [M][k] out;  topk_w fp32 [M][k] out
+ * The choice is exact: it is made on the logits, or on scores evaluated in 64
+ * bits, not on fp32 scores whose rounding would order close experts. Weights
+ * are fp32.
+ * An expert whose logit or bias is -infinity is never chosen and has no part in
+ * its group's rank; where fewer than k are left, the rest of the row is expert
+ * -1 (an invalid route) with weight 0. A NaN choice value ranks above every
+ * number, so it is chosen and its weights are NaN: a bad logit shows. M == 0 is
+ * a no-op.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (limits above), MOE_ERR_HIP. */
+MOE_API moe_status moe_route(const moe_route_desc* d, const void* logits, int64_t ld, const float* bias,
+                             int32_t* topk_ids, float* topk_w, hipStream_t stream);
+
+/* Gradient of moe_route's weights with respect to the logits, every element of
+ * dlogits written. The choice has none, so the bias and the groups have no part
+ * in it (d's group fields are checked alone).
+ *   topk_ids  [M][k] as moe_route wrote them: an ID outside [0, E) is no route
+ *             and its dtopk_w is not read; an ID named twice counts twice
+ *   dtopk_w   fp32 [M][k]
+ *   dlogits   [M][E] of out_dtype (the logits' or MOE_DTYPE_F32), stride ldd;
+ *             may not overlap the inputs
+ * Errors as moe_route. */
+MOE_API moe_status moe_route_grad(const moe_route_desc* d, const void* logits, int64_t ld, const int32_t* topk_ids,
+                                  const float* dtopk_w, int32_t out_dtype, void* dlogits, int64_t ldd,
+                                  hipStream_t stream);
+
+/* The inverse of an alignment: positions[r] = the aligned row that holds route
+ * r, -1 for a route without one; int32 [routes], from moe_align's
+ * sorted_route_ids (capacity entries, of which those below num_padded count;
+ * entries outside [0, routes) are padding) in any order. A route named twice gets
+ * one of its rows.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (more than 2^31 - 256 routes
+ * or rows), MOE_ERR_HIP. */
+MOE_API moe_status moe_align_positions(const int32_t* sorted_route_ids, const int32_t* num_padded, size_t capacity,
+                                       int32_t routes, int32_t* positions, hipStream_t stream);
+
+/* Step (4) on plain rows: the sum of a token's routes, with its gradient. Row
+ * operands are [..][H] with a stride of ld elements (>= H, a multiple of 8, at
+ * most 2^22) and 16-byte aligned. */
+typedef struct {
+  int32_t M;        /* tokens (>= 0) */
+  int32_t k;        /* routes per token (>= 1; M * k at most 2^31 - 256) */
+  int32_t H;        /* columns: a multiple of 8, at most 2^20 */
+  int32_t rows;     /* rows of `rows` and `drows` (0..2^31 - 256) */
+  int32_t dtype;    /* moe_dtype of rows and drows: MOE_DTYPE_F32, _BF16 or _F16 */
+  int32_t y_dtype;  /* moe_dtype of y and dy: any of the three */
+} moe_combine_desc;
+
+/* y[t] = sum_j topk_w[t][j] rows[positions[t][j]], fp32 sums in slot order,
+ * rounded once to y_dtype. A position outside [0, rows) is no row: its slot
+ * contributes nothing, whatever its weight.
+ *   positions  int32 [M][k] (moe_align_positions), or NULL: route r is row r
+ *   topk_w     fp32 [M][k], or NULL: ones (the gradient of a gather of tokens)
+ *   y          [M][H] (stride ldy)
+ * Errors of this and the next call: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED
+ * (limits above), MOE_ERR_HIP. */
+MOE_API moe_status moe_combine(const moe_combine_desc* d, const void* rows, int64_t ldr, const int32_t* positions,
+                               const float* topk_w, void* y, int64_t ldy, hipStream_t stream);
+
+/* Gradient of moe_combine: drows[positions[t][j]] = topk_w[t][j] dy[t] and
+ * dtopk_w[t][j] = rows[positions[t][j]] . dy[t] (0 for a slot without a row).
+ * Rows of drows that no slot names, padding among them, are left as they were.
+ * With topk_w NULL and dtopk_w NULL it is the gather of tokens into their
+ * routes' rows. Two slots may not name the same row.
+ *   rows     as there; not read, and may be NULL, when dtopk_w is NULL
+ *   drows    [rows][H] (stride lddr); may not overlap the inputs
+ *   dtopk_w  fp32 [M][k] out, or NULL */
+MOE_API moe_status moe_combine_grad(const moe_combine_desc* d, const void* dy, int64_t lddy, const void* rows,
+                                    int64_t ldr, const int32_t* positions, const float* topk_w, void* drows,
+                                    int64_t lddr, float* dtopk_w, hipStream_t stream);
+
+/* Products of a few rows with packed 4-bit weights, without the layer's
+ * activation: projections beside the experts (E = 1, topk_ids NULL), or the
+ * routed experts' own. */
+typedef struct {
+  int32_t M;          /* rows of x (>= 0) */
+  int32_t k;          /* rows of y per row of x (>= 1; 1 without topk_ids); M * k at most 2^31 - 256 */
+  int32_t E;          /* matrices (1..2048; 1 without topk_ids) */
+  int32_t N;          /* output features (1..2^20) */
+  int32_t K;          /* input features: a multiple of 32 and of w.group, at most 2^20 */
+  int32_t dtype;      /* moe_dtype of x: MOE_DTYPE_BF16 or _F16 */
+  int32_t out_dtype;  /* the same, or MOE_DTYPE_F32 */
+  moe_weights w;      /* MOE_W_INT4_AWQ [E][N][K]; zero NULL: 8 throughout. q 16-byte aligned */
+} moe_matvec_desc;
+
+/* y[t * k + j][n] = sum_i W[topk_ids[t][j]][n][i] x[t][i], W = (q - zero) * scale.
+ * Exact products, fp32 sums, rounded once to out_dtype. A row whose ID lies
+ * outside [0, E) becomes zero. M == 0 is a no-op.
+ *   x         [M][K] (stride ldx: a multiple of 8, at most 2^22; 16-byte aligned)
+ *   topk_ids  int32 [M][k], or NULL
+ *   y         [M * k][N] (stride ldy >= N, at most 2^22); not overlapping inputs
+ * Weights are read once per 64 rows without topk_ids, once per row with them.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (limits, MXFP8 weights,
+ * more than 2^40 outputs), MOE_ERR_HIP. */
+MOE_API moe_status moe_matvec_int4(const moe_matvec_desc* d, const void* x, int64_t ldx, const int32_t* topk_ids,
+                                   void* y, int64_t ldy, hipStream_t stream);
+
 /* Number of kernels moe_ffn_forward launches for this description (0 on error). */
 MOE_API int32_t moe_ffn_kernel_count(const moe_ffn_desc* d);
 

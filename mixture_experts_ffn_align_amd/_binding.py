@@ -37,10 +37,14 @@ MOE_DTYPE_BF16 = 1
 MOE_DTYPE_F16 = 2
 MOE_DTYPE_MXFP4 = 3
 
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+
 _c_i32 = ctypes.c_int32
 _c_i64 = ctypes.c_int64
 _c_size = ctypes.c_size_t
 _c_ptr = ctypes.c_void_p
+_c_float = ctypes.c_float
 
 
 class moe_weights(ctypes.Structure):
@@ -57,6 +61,22 @@ class moe_ffn_desc(ctypes.Structure):
 class moe_grouped_matmul_desc(ctypes.Structure):
     _fields_ = [("rows", _c_i32), ("E", _c_i32), ("N", _c_i32), ("K", _c_i32), ("dtype", _c_i32),
                 ("out_dtype", _c_i32)]
+
+
+class moe_route_desc(ctypes.Structure):
+    _fields_ = [("M", _c_i32), ("E", _c_i32), ("k", _c_i32), ("dtype", _c_i32), ("score", _c_i32),
+                ("renormalize", _c_i32), ("scale", _c_float), ("groups", _c_i32), ("topk_groups", _c_i32),
+                ("group_top", _c_i32)]
+
+
+class moe_combine_desc(ctypes.Structure):
+    _fields_ = [("M", _c_i32), ("k", _c_i32), ("H", _c_i32), ("rows", _c_i32), ("dtype", _c_i32),
+                ("y_dtype", _c_i32)]
+
+
+class moe_matvec_desc(ctypes.Structure):
+    _fields_ = [("M", _c_i32), ("k", _c_i32), ("E", _c_i32), ("N", _c_i32), ("K", _c_i32), ("dtype", _c_i32),
+                ("out_dtype", _c_i32), ("w", moe_weights)]
 
 
 class MoeError(RuntimeError):
@@ -105,6 +125,15 @@ _SIGNATURES = {
     "moe_mxfp4_quantize": (_c_i32, [_c_i32, _c_ptr, _c_i64, _c_i64, _c_i32, _c_ptr, _c_ptr, _c_ptr]),
     "moe_mxfp4_dequantize": (_c_i32, [_c_i32, _c_ptr, _c_ptr, _c_i64, _c_i32, _c_ptr, _c_i64, _c_ptr]),
     "moe_align_offsets": (_c_i32, [_c_ptr, _c_ptr, _c_size, _c_i32, _c_i32, _c_ptr, _c_ptr]),
+    "moe_route": (_c_i32, [ctypes.POINTER(moe_route_desc), _c_ptr, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr]),
+    "moe_route_grad": (_c_i32, [ctypes.POINTER(moe_route_desc), _c_ptr, _c_i64, _c_ptr, _c_ptr, _c_i32, _c_ptr,
+                                _c_i64, _c_ptr]),
+    "moe_align_positions": (_c_i32, [_c_ptr, _c_ptr, _c_size, _c_i32, _c_ptr, _c_ptr]),
+    "moe_combine": (_c_i32, [ctypes.POINTER(moe_combine_desc), _c_ptr, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64,
+                             _c_ptr]),
+    "moe_combine_grad": (_c_i32, [ctypes.POINTER(moe_combine_desc), _c_ptr, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_ptr,
+                                  _c_ptr, _c_i64, _c_ptr, _c_ptr]),
+    "moe_matvec_int4": (_c_i32, [ctypes.POINTER(moe_matvec_desc), _c_ptr, _c_i64, _c_ptr, _c_ptr, _c_i64, _c_ptr]),
     "moe_ffn_kernel_count": (_c_i32, [ctypes.POINTER(moe_ffn_desc)]),
     "moe_ffn_kernel_name": (ctypes.c_char_p, [ctypes.POINTER(moe_ffn_desc), _c_i32]),
     "moe_ffn_intermediate": (_c_i32, [ctypes.POINTER(moe_ffn_desc), ctypes.POINTER(_c_size),
@@ -680,4 +709,220 @@ def moe_align_offsets(expert_block_ids, num_padded, E: int, b: int, offsets, str
                   offsets.data_ptr())
     if check:
         _check(st, "moe_align_offsets")
+    return st
+
+
+# ---------------------------------------------------------------------------
+# Routing, the weighted sum of routes, products with packed 4-bit weights
+# ---------------------------------------------------------------------------
+
+def _expect_2d(name, t):
+    if not hasattr(t, "data_ptr"):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected 2 dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _expect_logits(name, t, shape, device=None):
+    """_expect_rows without its rule for one row: any stride from the row's length on."""
+    ld = _expect_rows(name, t, shape, device)
+    return ld if shape[0] > 1 else shape[1]
+
+
+def _route_desc(M, E, k, dtype, score, renormalize, scale, groups, topk_groups, group_top):
+    if not 0 <= groups | topk_groups | group_top | score | M | E <= _I32_MAX:
+        _expect_i32(M=M, E=E, score=score, groups=groups, topk_groups=topk_groups, group_top=group_top)
+    return moe_route_desc(M, E, k, dtype, score, 1 if renormalize else 0, scale, groups, topk_groups, group_top)
+
+
+def moe_route(logits, topk_ids, topk_w, bias=None, score: int = MOE_SCORE_SOFTMAX, renormalize: bool = True,
+              scale: float = 1.0, groups: int = 1, topk_groups: int = 1, group_top: int = 1, stream=None,
+              check: bool = True) -> int:
+    """Routes tokens to experts: topk_ids [M, k] int32 and topk_w [M, k] fp32 of logits
+    [M, E] (bf16, fp16 or fp32; may have a row stride).
+
+    The score is softmax or sigmoid (MOE_SCORE_*), the choice by score + bias ([E] fp32,
+    or None), within the topk_groups of `groups` groups whose group_top largest values
+    sum highest; weights are scale * score, divided by the chosen scores' sum with
+    renormalize. Ties go to the lowest index; experts at -inf are never chosen, and
+    where fewer than k are left the rest is expert -1 with weight 0."""
+    M, E = _expect_2d("logits", logits)
+    dt = _dtype_code("logits", logits, _ALL_TYPES)
+    ld = _expect_logits("logits", logits, (M, E))
+    dev = logits.device
+    k = topk_ids.shape[1] if hasattr(topk_ids, "data_ptr") and topk_ids.dim() == 2 else -1
+    _expect_like("topk_ids", topk_ids, torch.int32, (M, k), dev)
+    _expect_like("topk_w", topk_w, torch.float32, (M, k), dev)
+    b = None
+    if bias is not None:
+        _expect_like("bias", bias, torch.float32, (E,), dev)
+        b = bias.data_ptr()
+    d = _route_desc(M, E, k, dt, score, renormalize, scale, groups, topk_groups, group_top)
+    st = _call_on(dev, stream, lib().moe_route, ctypes.byref(d), logits.data_ptr(), ld, b, topk_ids.data_ptr(),
+                  topk_w.data_ptr())
+    if check:
+        _check(st, "moe_route")
+    return st
+
+
+def moe_route_grad(logits, topk_ids, dtopk_w, dlogits, score: int = MOE_SCORE_SOFTMAX, renormalize: bool = True,
+                   scale: float = 1.0, stream=None, check: bool = True) -> int:
+    """Gradient of moe_route's weights with respect to the logits: dlogits [M, E] (the
+    logits' dtype or fp32; may have a row stride) from topk_ids as moe_route wrote them
+    and dtopk_w [M, k] fp32. The choice has no gradient, so bias and groups have no part
+    in it."""
+    M, E = _expect_2d("logits", logits)
+    dt = _dtype_code("logits", logits, _ALL_TYPES)
+    out = _dtype_code("dlogits", dlogits, (dt, MOE_DTYPE_F32))
+    ld = _expect_logits("logits", logits, (M, E))
+    dev = logits.device
+    k = topk_ids.shape[1] if hasattr(topk_ids, "data_ptr") and topk_ids.dim() == 2 else -1
+    _expect_like("topk_ids", topk_ids, torch.int32, (M, k), dev)
+    _expect_like("dtopk_w", dtopk_w, torch.float32, (M, k), dev)
+    ldd = _expect_logits("dlogits", dlogits, (M, E), dev)
+    d = _route_desc(M, E, k, dt, score, renormalize, scale, 1, 1, 1)
+    st = _call_on(dev, stream, lib().moe_route_grad, ctypes.byref(d), logits.data_ptr(), ld, topk_ids.data_ptr(),
+                  dtopk_w.data_ptr(), out, dlogits.data_ptr(), ldd)
+    if check:
+        _check(st, "moe_route_grad")
+    return st
+
+
+def moe_align_positions(sorted_route_ids, num_padded, positions, stream=None, check: bool = True) -> int:
+    """The inverse of an alignment: positions [M, k] int32, the row of each route in
+    moe_align's sorted_route_ids (-1 for a route without one)."""
+    if not hasattr(sorted_route_ids, "data_ptr"):
+        raise TypeError(f"sorted_route_ids: expected a torch.Tensor, got {type(sorted_route_ids).__name__}")
+    n = sorted_route_ids.numel()
+    dev = sorted_route_ids.device
+    if dev.type != "cuda":
+        _expect("sorted_route_ids", sorted_route_ids, torch.int32, (n,))
+    _expect_like("sorted_route_ids", sorted_route_ids, torch.int32, (n,), dev)
+    _expect_like("num_padded", num_padded, torch.int32, (1,), dev)
+    _expect_like("positions", positions, torch.int32, _expect_2d("positions", positions), dev)
+    routes = positions.numel()
+    if routes > _I32_MAX:
+        _expect_i32(routes=routes)
+    st = _call_on(dev, stream, lib().moe_align_positions, sorted_route_ids.data_ptr(), num_padded.data_ptr(), n,
+                  routes, positions.data_ptr())
+    if check:
+        _check(st, "moe_align_positions")
+    return st
+
+
+def _slots(positions, topk_w, M, rows, device):
+    """(k, pointers of positions and topk_w) of a combine call. Without both, each
+    token has the rows' share of it: rows / M routes."""
+    if positions is not None:
+        k = positions.shape[1] if hasattr(positions, "data_ptr") and positions.dim() == 2 else -1
+        _expect_like("positions", positions, torch.int32, (M, k), device)
+    elif topk_w is not None:
+        k = topk_w.shape[1] if hasattr(topk_w, "data_ptr") and topk_w.dim() == 2 else -1
+    else:
+        k = rows // M if M > 0 else 1
+    if topk_w is not None:
+        _expect_like("topk_w", topk_w, torch.float32, (M, k), device)
+    if positions is None and rows != M * k:
+        raise ValueError(f"positions: needed for {rows} rows of {M} x {k} routes")
+    return k, None if positions is None else positions.data_ptr(), None if topk_w is None else topk_w.data_ptr()
+
+
+def moe_combine(rows, positions, topk_w, y, stream=None, check: bool = True) -> int:
+    """y[t] = sum_j topk_w[t, j] rows[positions[t, j]].
+
+    rows [R, H] and y [M, H] bf16, fp16 or fp32 (each may have a row stride), positions
+    [M, k] int32 (moe_align_positions; outside [0, R): no row) or None (route t * k + j is
+    that row), topk_w [M, k] fp32 or None (ones)."""
+    R, H = _expect_2d("rows", rows)
+    dt = _dtype_code("rows", rows, _ALL_TYPES)
+    out = _dtype_code("y", y, _ALL_TYPES)
+    ldr = _expect_rows("rows", rows, (R, H))
+    dev = rows.device
+    M = y.shape[0] if y.dim() == 2 else -1
+    ldy = _expect_rows("y", y, (M, H), dev)
+    k, pos, w = _slots(positions, topk_w, M, R, dev)
+    if M > _I32_MAX or R > _I32_MAX or H > _I32_MAX:
+        _expect_i32(M=M, rows=R, H=H)
+    d = moe_combine_desc(M, k, H, R, dt, out)
+    st = _call_on(dev, stream, lib().moe_combine, ctypes.byref(d), rows.data_ptr(), ldr, pos, w, y.data_ptr(), ldy)
+    if check:
+        _check(st, "moe_combine")
+    return st
+
+
+def moe_combine_grad(dy, rows, positions, topk_w, drows, dtopk_w, stream=None, check: bool = True) -> int:
+    """Gradient of moe_combine: drows[positions[t, j]] = topk_w[t, j] dy[t] and
+    dtopk_w[t, j] = rows[positions[t, j]] . dy[t].
+
+    dy [M, H], drows [R, H] of the rows' dtype, dtopk_w [M, k] fp32 or None (rows are not
+    read then and may be None). With topk_w and dtopk_w None it gathers tokens into their
+    routes' rows. Rows no slot names are left as they were."""
+    R, H = _expect_2d("drows", drows)
+    dt = _dtype_code("drows", drows, _ALL_TYPES)
+    ydt = _dtype_code("dy", dy, _ALL_TYPES)
+    lddr = _expect_rows("drows", drows, (R, H))
+    dev = drows.device
+    M = dy.shape[0] if dy.dim() == 2 else -1
+    lddy = _expect_rows("dy", dy, (M, H), dev)
+    k, pos, w = _slots(positions, topk_w, M, R, dev)
+    ldr, src, dw = 0, None, None
+    if dtopk_w is not None:
+        _dtype_code("rows", rows, (dt,))
+        ldr = _expect_rows("rows", rows, (R, H), dev)
+        src = rows.data_ptr()
+        _expect_like("dtopk_w", dtopk_w, torch.float32, (M, k), dev)
+        dw = dtopk_w.data_ptr()
+    if M > _I32_MAX or R > _I32_MAX or H > _I32_MAX:
+        _expect_i32(M=M, rows=R, H=H)
+    d = moe_combine_desc(M, k, H, R, dt, ydt)
+    st = _call_on(dev, stream, lib().moe_combine_grad, ctypes.byref(d), dy.data_ptr(), lddy, src, ldr, pos, w,
+                  drows.data_ptr(), lddr, dw)
+    if check:
+        _check(st, "moe_combine_grad")
+    return st
+
+
+def moe_matvec_int4(x, w, y, topk_ids=None, stream=None, check: bool = True) -> int:
+    """Products of a few rows with packed 4-bit weights: y[t] = W x[t], or with topk_ids
+    [M, k] int32 y[t, j] = W[topk_ids[t, j]] x[t] (zero for an ID outside [0, E)).
+
+    x [M, K] bf16 or fp16 (may have a row stride), w a DeviceProjection of int4 weights
+    (q int32 [E, N, K / 8], scale fp16 or its int16 bits [E, N, K / group], zero uint8 as
+    scale or None: 8), y of x's dtype or fp32: [M, N] (may have a row stride), or
+    [M, k, N]."""
+    M, K = _expect_2d("x", x)
+    dt = _dtype_code("x", x, _GMM_TYPES)
+    out = _dtype_code("y", y, (dt, MOE_DTYPE_F32))
+    ldx = _expect_rows("x", x, (M, K))
+    dev = x.device
+    if not hasattr(w, "zero"):
+        raise TypeError(f"w: expected a DeviceProjection, got {type(w).__name__}")
+    q, scale, zero, group = w.q, w.scale, w.zero, w.group
+    E, N, words = _expect_3d("q", q)
+    if words * 8 != K:
+        raise ValueError(f"q: expected shape {(E, N, K // 8)}, got {tuple(q.shape)}")
+    _expect_like("q", q, torch.int32, (E, N, words), dev)
+    parts = (E, N, K // group if group > 0 else 0)
+    _expect_like("scale", scale, torch.float16 if getattr(scale, "dtype", None) is torch.float16 else torch.int16,
+                 parts, dev)
+    z = None
+    if zero is not None:
+        _expect_like("zero", zero, torch.uint8, parts, dev)
+        z = zero.data_ptr()
+    if topk_ids is None:
+        k, ids = 1, None
+        ldy = _expect_rows("y", y, (M, N), dev)
+        ldy = ldy if M > 1 else N
+    else:
+        k = topk_ids.shape[1] if hasattr(topk_ids, "data_ptr") and topk_ids.dim() == 2 else -1
+        _expect_like("topk_ids", topk_ids, torch.int32, (M, k), dev)
+        ids, ldy = topk_ids.data_ptr(), N
+        _expect_like("y", y, y.dtype, (M, k, N), dev)
+    if M > _I32_MAX or K > _I32_MAX or N > _I32_MAX or E > _I32_MAX or group > _I32_MAX:
+        _expect_i32(M=M, K=K, N=N, E=E, group=group)
+    d = moe_matvec_desc(M, k, E, N, K, dt, out, moe_weights(w.fmt, group, q.data_ptr(), scale.data_ptr(), z))
+    st = _call_on(dev, stream, lib().moe_matvec_int4, ctypes.byref(d), x.data_ptr(), ldx, ids, y.data_ptr(), ldy)
+    if check:
+        _check(st, "moe_matvec_int4")
     return st

@@ -128,6 +128,63 @@ hipError_t launch_mxfp4_quantize(int dtype, const void* x, int64_t ldx, int64_t 
 hipError_t launch_mxfp4_dequantize(int dtype, const void* q, const uint8_t* scale, int64_t rows, int K, void* y,
                                    int64_t ldy, hipStream_t stream);
 
+// Routing (route.hip). ld, ldd in elements.
+struct RouteArgs {
+  const void* logits;
+  const float* bias;        // or null
+  int32_t* topk_ids;
+  float* topk_w;
+  int64_t ld, M;
+  int E, k, dtype, score;
+  bool renormalize, exact_scores;
+  float scale;
+  int groups, topk_groups, group_top;
+  int group_size, per_group, per_lane;   // set by launch_route
+};
+hipError_t launch_route(const RouteArgs& p, hipStream_t stream);
+
+struct RouteGradArgs {
+  const void* logits;
+  const int32_t* topk_ids;
+  const float* dtopk_w;
+  void* dlogits;
+  int64_t ld, ldd, M;
+  int E, k, dtype, out_dtype, score;
+  bool renormalize;
+  float scale;
+};
+hipError_t launch_route_grad(const RouteGradArgs& p, hipStream_t stream);
+
+// The weighted sum of routes (combine.hip); strides in elements.
+struct CombineArgs {
+  const void* rows;          // [rows_n][H]
+  const int32_t* positions;  // [M * k], or null: route r in row r
+  const float* topk_w;       // [M * k], or null: ones
+  void* y;                   // [M][H]
+  const void* dy;            // gradient of y
+  void* drows;
+  float* dtopk_w;            // or null
+  int64_t ldr, ldy, lddr;    // ldy: of y or dy
+  int64_t M, rows_n;
+  int k, H;
+};
+hipError_t launch_combine_rows(const CombineArgs& p, int dtype, int y_dtype, hipStream_t stream);
+hipError_t launch_combine_grad(const CombineArgs& p, int dtype, int y_dtype, hipStream_t stream);
+hipError_t launch_positions(const int32_t* sorted, const int32_t* num_padded, int capacity, int routes,
+                            int32_t* positions, hipStream_t stream);
+
+// Products with packed 4-bit weights (matvec.hip).
+struct MatvecArgs {
+  const void* x;             // row r of y reads row r / per
+  const int32_t* ids;        // [rows], or null: one matrix
+  void* y;
+  moe_weights w;
+  int64_t ldx, ldy, rows;
+  int64_t tasks;             // set by launch_matvec
+  int per, E, N, K, group, out_dtype;
+};
+hipError_t launch_matvec(const MatvecArgs& p, int dtype, hipStream_t stream);
+
 // Row offsets of an alignment (align.hip).
 hipError_t launch_align_offsets(const int32_t* blocks, const int32_t* num_padded, int nblk, int E, int b,
                                 int32_t* offsets, hipStream_t stream);

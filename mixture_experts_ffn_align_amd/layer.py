@@ -1,4 +1,4 @@
-"""Device-resident expert weights and a layer object over the C ABI.
+"""Device-resident expert weights, a router and a layer object over the C ABI.
 
 Holds the packed weights as torch device tensors (memory only), sizes the
 workspace with moe_ffn_workspace_size and calls moe_ffn_forward on the
@@ -46,6 +46,31 @@ class DeviceProjection:
         if self.zero is not None:
             n += self.zero.numel() * self.zero.element_size()
         return n
+
+
+class MoeRouter:
+    """Routing with fixed settings (moe_route's): logits [M, E] to what MoeLayer.forward
+    takes, layer.forward(x, *router(logits))."""
+
+    def __init__(self, k: int, score: int = B.MOE_SCORE_SOFTMAX, bias: torch.Tensor | None = None,
+                 renormalize: bool = True, scale: float = 1.0, groups: int = 1, topk_groups: int = 1,
+                 group_top: int = 1):
+        self.k, self.bias = k, bias
+        self.weights = dict(score=score, renormalize=renormalize, scale=scale)
+        self.choice = dict(groups=groups, topk_groups=topk_groups, group_top=group_top)
+
+    def __call__(self, logits: torch.Tensor):
+        """(topk_ids [M, k] int32, topk_w [M, k] fp32)."""
+        ids = torch.empty((logits.shape[0], self.k), dtype=torch.int32, device=logits.device)
+        w = torch.empty((logits.shape[0], self.k), dtype=torch.float32, device=logits.device)
+        B.moe_route(logits, ids, w, self.bias, **self.weights, **self.choice)
+        return ids, w
+
+    def grad(self, logits: torch.Tensor, topk_ids: torch.Tensor, dtopk_w: torch.Tensor) -> torch.Tensor:
+        """Gradient of the weights with respect to the logits, of the logits' dtype."""
+        d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        B.moe_route_grad(logits, topk_ids, dtopk_w, d, **self.weights)
+        return d
 
 
 class MoeLayer:

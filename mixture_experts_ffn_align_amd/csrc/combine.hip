@@ -14,7 +14,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSlots = 8;              // routes whose loads are in flight together
 constexpr int kPositionThreads = 1024;
-constexpr int kPositionsSingle = 32768;   // routes and rows up to which one workgroup inverts the alignment
+constexpr int kPositionsSingle = 8192;    // routes and rows up to which one workgroup inverts the alignment
 
 typedef float floatx8 __attribute__((ext_vector_type(8)));
 typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
@@ -162,9 +162,14 @@ __global__ __launch_bounds__(kThreads) void combine_grad(CombineArgs p) {
 // scatter: by a barrier in one workgroup, by a second launch in several.
 __device__ __forceinline__ void scatter_positions(const int32_t* sorted, int live, int routes, int32_t* positions,
                                                   int first, int step) {
-  for (int64_t i = first; i < live; i += step) {
-    const int r = sorted[i];
-    if (r >= 0 && r < routes) positions[r] = static_cast<int>(i);
+  constexpr int kBatch = 4;                 // loads in flight
+  for (int64_t i = first; i < live; i += int64_t(kBatch) * step) {
+    int r[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) r[q] = i + int64_t(q) * step < live ? sorted[i + int64_t(q) * step] : -1;
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q)
+      if (r[q] >= 0 && r[q] < routes) positions[r[q]] = static_cast<int>(i + int64_t(q) * step);
   }
 }
 
@@ -241,7 +246,7 @@ hipError_t launch_positions(const int32_t* sorted, const int32_t* num_padded, in
     const int fill = (routes + kPositionThreads - 1) / kPositionThreads;
     const int scatter = (capacity + kPositionThreads - 1) / kPositionThreads;
     launch(positions_fill, dim3(min(fill, 1024)), dim3(kPositionThreads), 0, stream, routes, positions);
-    launch(positions_scatter, dim3(min(max(scatter, 1), 1024)), dim3(kPositionThreads), 0, stream, sorted, num_padded,
+    launch(positions_scatter, dim3(min(max(scatter / 4, 1), 1024)), dim3(kPositionThreads), 0, stream, sorted, num_padded,
            capacity, routes, positions);
   }
   return hipGetLastError();

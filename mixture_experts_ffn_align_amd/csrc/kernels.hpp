@@ -129,6 +129,9 @@ hipError_t launch_mxfp4_dequantize(int dtype, const void* q, const uint8_t* scal
                                    int64_t ldy, hipStream_t stream);
 
 // Routing (route.hip). ld, ldd in elements.
+struct RouteLayout {         // how a row's experts are dealt to lanes
+  int per_group, per_lane;
+};
 struct RouteArgs {
   const void* logits;
   const float* bias;        // or null
@@ -136,10 +139,14 @@ struct RouteArgs {
   float* topk_w;
   int64_t ld, M;
   int E, k, dtype, score;
-  bool renormalize, exact_scores;
+  bool renormalize;
   float scale;
   int groups, topk_groups, group_top;
-  int group_size, per_group, per_lane;   // set by launch_route
+  // Set by launch_route:
+  int group_size;
+  RouteLayout wide, narrow;  // over 64 and over 16 lanes
+  bool exact_scores;         // the choice takes scores, not logits alone
+  bool vector;               // rows are read in 16-byte pieces
 };
 hipError_t launch_route(const RouteArgs& p, hipStream_t stream);
 

@@ -9,6 +9,8 @@
 // The choice is made on 64-bit values: an fp32 evaluation would order close
 // experts by its own rounding, and the same token would take other routes in
 // another kernel, batch or framework. The weights are fp32.
+#include <type_traits>
+
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -62,130 +64,428 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-// A wave takes a row. Lanes are dealt to groups (`per_group` of them each, a
-// power of two), a lane owns C consecutive experts of its group at most, so
-// that experts ascend with (lane, place).
-template <int C>
-__global__ __launch_bounds__(kThreads) void route(RouteArgs p) {
+// How the experts of a row are dealt to `lanes` lanes: `per_group` of them (a
+// power of two) to each group, each with `per_lane` consecutive experts of it at
+// most, so that experts ascend with (lane, place).
+struct Deal {
+  int group, first, end;
+};
+__device__ __forceinline__ Deal deal(const RouteLayout& y, int lane, int groups, int group_size) {
+  Deal d;
+  d.group = lane / y.per_group;
+  d.first = d.group * group_size + (lane % y.per_group) * y.per_lane;
+  d.end = d.group < groups ? min(d.first + y.per_lane, (d.group + 1) * group_size) : d.first;
+  return d;
+}
+
+// The weight of this lane's slot (expert `mine`, or -1), before p.scale; `top` and
+// `total` are the largest logit and the softmax's sum relative to it. kMax and
+// kSum reduce over the lanes that hold the row's slots.
+template <typename Max, typename Sum>
+__device__ __forceinline__ float weight_of(const RouteArgs& p, int mine, float chosen, float top, float total, Max kMax,
+                                           Sum kSum) {
+  if (p.renormalize) {
+    // Relative to the largest chosen score, so that small scores do not vanish.
+    float m = kMax(mine >= 0 ? chosen : -INFINITY);
+    float s;
+    if (p.score == MOE_SCORE_SOFTMAX) {
+      s = mine >= 0 ? expf(chosen - m) : 0.0f;
+    } else {
+      m = fminf(m, 0.0f);
+      s = mine >= 0 ? expf(fminf(chosen, 0.0f) - m) / (1.0f + expf(-fabsf(chosen))) : 0.0f;
+    }
+    return s / kSum(s);
+  }
+  return p.score == MOE_SCORE_SOFTMAX ? expf(chosen - top) / total : 1.0f / (1.0f + expf(-chosen));
+}
+
+// The lanes of a wave exchange through LDS without a barrier: its accesses stay in order.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// One row by a whole wave, every choice value in 64 bits and kept in LDS (E
+// keys): any sizes, and the rows that `route_narrow` cannot decide.
+__device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t row, int64_t* key) {
   const int lane = threadIdx.x & (kWave - 1);
-  const int group = lane / p.per_group;
-  const int first = group * p.group_size + (lane % p.per_group) * p.per_lane;
-  const int end = group < p.groups ? min(first + p.per_lane, (group + 1) * p.group_size) : first;
-  for (int64_t row = blockIdx.x * int64_t(kWaves) + threadIdx.x / kWave; row < p.M; row += int64_t(gridDim.x) * kWaves) {
+  const int64_t at = row * p.ld;
+  const auto logit = [&](int e) { return load_elem(p.logits, at + e, p.dtype); };
+  float top = -INFINITY, total = 0.0f;      // of the softmax, relative to `top`
+  double total64 = 0.0;
+  if (p.score == MOE_SCORE_SOFTMAX) {
+    for (int e = lane; e < p.E; e += kWave) top = fmaxf(top, logit(e));
+    top = wave_max(top);
+    for (int e = lane; e < p.E; e += kWave) {
+      const float l = logit(e);
+      if (l == -INFINITY) continue;
+      if (!p.renormalize) total += expf(l - top);
+      if (p.exact_scores) total64 += exp(static_cast<double>(l) - top);
+    }
+    total = wave_sum(total);
+    total64 = wave_sum64(total64);
+  }
+  // Keys of the choice values; of the scores alone, where those are summed over groups without a bias.
+  for (int e = lane; e < p.E; e += kWave) {
+    const float l = logit(e), b = p.bias != nullptr ? p.bias[e] : 0.0f;
+    double s = l;
+    if (p.exact_scores) s = (p.score == MOE_SCORE_SOFTMAX ? exp(s - top) / total64 : 1.0 / (1.0 + exp(-s))) + b;
+    key[e] = l == -INFINITY || b == -INFINITY ? kNoKey : key_of(s);
+  }
+  wave_lds_fence();
+  if (p.topk_groups < p.groups) {
+    const Deal d = deal(p.wide, lane, p.groups, p.group_size);
+    int64_t a = kNoKey, b = kNoKey;         // the two largest of the group
+    for (int e = d.first; e < d.end; ++e) {
+      b = max(b, min(a, key[e]));
+      a = max(a, key[e]);
+    }
+    for (int off = 1; off < p.wide.per_group; off <<= 1) {
+      const int64_t oa = __shfl_xor(a, off, kWave), ob = __shfl_xor(b, off, kWave);
+      b = max(min(a, oa), max(b, ob));
+      a = max(a, oa);
+    }
+    int64_t g = a;
+    if (p.group_top == 2 && a != kNanKey && b != kNoKey) g = key_of(value_of(a) + value_of(b));
+    int rank = 0;
+    for (int o = 0; o < p.groups; ++o) {
+      const int64_t og = __shfl(g, o * p.wide.per_group, kWave);
+      rank += (og > g || (og == g && o < d.group)) ? 1 : 0;
+    }
+    for (int e = d.first; e < d.end; ++e) {
+      if (rank >= p.topk_groups)
+        key[e] = kNoKey;
+      else if (p.bias == nullptr && p.exact_scores && key[e] != kNoKey)
+        key[e] = key_of(logit(e));
+    }
+    wave_lds_fence();
+  }
+  int mine = -1;                            // expert of slot `lane`
+  for (int j = 0; j < p.k; ++j) {
+    int64_t best = kNoKey;
+    int e = INT32_MAX;
+    for (int i = lane; i < p.E; i += kWave) {
+      const int64_t t = key[i];
+      if (t > best) {
+        best = t;
+        e = i;
+      }
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+      const int64_t ob = __shfl_xor(best, off, kWave);
+      const int oe = __shfl_xor(e, off, kWave);
+      if (ob > best || (ob == best && oe < e)) {
+        best = ob;
+        e = oe;
+      }
+    }
+    if (best == kNoKey) break;
+    if (lane == j) mine = e;
+    if (lane == 0) key[e] = kNoKey;
+    wave_lds_fence();
+  }
+  const float chosen = mine >= 0 ? logit(mine) : -INFINITY;
+  const float s = weight_of(p, mine, chosen, top, total, [](float v) { return wave_max(v); },
+                            [](float v) { return wave_sum(v); });
+  if (lane < p.k) {
+    p.topk_ids[row * p.k + lane] = mine;
+    p.topk_w[row * p.k + lane] = mine >= 0 ? p.scale * s : 0.0f;
+  }
+  wave_lds_fence();
+}
+
+__global__ __launch_bounds__(kThreads) void route_wide(RouteArgs p) {
+  extern __shared__ int64_t keys[];
+  for (int64_t row = blockIdx.x * int64_t(kWaves) + threadIdx.x / kWave; row < p.M; row += int64_t(gridDim.x) * kWaves)
+    route_exact(p, row, keys + threadIdx.x / kWave * p.E);
+}
+
+constexpr int kLanes = 16;                 // of a row in route_narrow
+constexpr int kRows = kThreads / kLanes;
+
+// A value of another of the row's sixteen lanes (rotated by kBy).
+template <int kBy>
+__device__ __forceinline__ float ror(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 | kBy, 0xF, 0xF, false));
+}
+template <int kBy>
+__device__ __forceinline__ int ror(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, 0x120 | kBy, 0xF, 0xF, false);
+}
+
+// Reductions over a row's sixteen lanes; every lane ends with the same bits.
+template <typename V>
+__device__ __forceinline__ V row_max(V v) {
+  v = max(v, ror<8>(v));
+  v = max(v, ror<4>(v));
+  v = max(v, ror<2>(v));
+  return max(v, ror<1>(v));
+}
+template <typename V>
+__device__ __forceinline__ V row_sum(V v) {
+  v += ror<8>(v);
+  v += ror<4>(v);
+  v += ror<2>(v);
+  return v + ror<1>(v);
+}
+
+// The value of a lane's partner in the merge of 2, 4, 8 and 16 lanes, when the
+// halves that are merged hold the same values in all their lanes.
+template <int kStep, typename V>
+__device__ __forceinline__ V partner(V v) {
+  constexpr int kCtrl = kStep == 1 ? 0xB1 : kStep == 2 ? 0x4E : kStep == 4 ? 0x141 : 0x140;
+  const int i = __builtin_bit_cast(int, v);
+  return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, i, kCtrl, 0xF, 0xF, false));
+}
+
+template <typename V>
+__device__ __forceinline__ V none();      // below every value
+template <>
+__device__ __forceinline__ float none<float>() { return -INFINITY; }
+template <>
+__device__ __forceinline__ int none<int>() { return INT32_MIN; }
+
+// Ordered 32-bit key of a logit, as key_of.
+__device__ __forceinline__ int key32(float v) {
+  if (v == -INFINITY) return INT32_MIN;
+  if (v != v) return INT32_MAX;
+  const int b = __float_as_int(v + 0.0f);
+  return b ^ ((b >> 31) & INT32_MAX);
+}
+
+// The sum of the values of the row's lanes before this one.
+__device__ __forceinline__ int row_before(int v) {
+  int x = v;
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true);
+  return x - v;
+}
+
+// e^x from the hardware's 2^x: within |x| 2^-23 + 2^-22 of it, relatively.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+// Sixteen lanes take a row, so a wave chooses for four at once. Values to rank
+// by: ordered keys of the logits, which are exact, or with a bias fp32 choice
+// values c = s + b, off by err + |c| 2^-24 at most. err: a sigmoid moves by
+// s (1 - s) |x| 2^-23 < 2^-25 through fast_exp's argument and by 2^-22 with its
+// roundings, for which 2^-21 stands; a softmax by its own and its sum's share,
+// (6.3 + 0.4) 2^-23 (the mean distance to the largest of 512 logits is below their
+// entropy's bound, ln 512) and 36 additions of 2^-24, for which 2^-18 stands.
+//   1. every lane finds the two largest of its C values;
+//   2. groups are ranked by them; two fp32 ranks that are too close decide nothing;
+//   3. the k-th largest T of all lanes' two largest bounds the k-th largest of the
+//      row from below and near: what is below T, less the errors, is out;
+//   4. the rest, a few more than k, go one to a lane (through LDS, in index order),
+//      are ranked by exact 64-bit values by counting, and those below k are chosen.
+// A row that step 2 leaves open, or with more than sixteen values left in step 4
+// (many equal values with a bias), goes to route_exact.
+template <int C, bool kBias>
+__global__ __launch_bounds__(kThreads) void route_narrow(RouteArgs p) {
+  extern __shared__ int64_t keys[];         // for route_exact
+  using V = std::conditional_t<kBias, float, int>;
+  struct Row {
+    union {
+      V top[2 * kLanes];
+      int64_t key[kLanes];
+    };
+    int id[kLanes];
+    float logit[kLanes];
+    uint32_t apart[4];                     // the four rows of a wave start in different banks
+  };
+  __shared__ __attribute__((aligned(16))) Row lds[kRows];
+  const float err = p.score == MOE_SCORE_SIGMOID ? 0x1p-21f : 0x1p-18f;
+  Row& mem = lds[threadIdx.x / kLanes];
+  for (int64_t row0 = blockIdx.x * int64_t(kRows); row0 < p.M; row0 += int64_t(gridDim.x) * kRows) {
+    // Opaque, or the compiler keeps what depends on it alone in (spilled) scalars across rows.
+    const int lane = in_vgpr(threadIdx.x % kLanes);
+    const Deal d = deal(p.narrow, lane, p.groups, p.group_size);
+    const int64_t row = row0 + threadIdx.x / kLanes;
+    const bool here = row < p.M;
     const int64_t at = row * p.ld;
     float l[C];
-    bool live[C];
-    float top = -INFINITY;
+    if (p.vector && here) {
+      const int64_t first = at + d.first;
+      if (p.dtype == MOE_DTYPE_F32) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const bool here = first + i < end;
-      l[i] = here ? load_elem(p.logits, at + first + i, p.dtype) : -INFINITY;
-      live[i] = here && !(l[i] == -INFINITY);
-      top = fmaxf(top, l[i]);
-    }
-    top = wave_max(top);
-    float total = 0.0f;       // of the softmax, relative to `top`
-    if (p.score == MOE_SCORE_SOFTMAX && !p.renormalize) {
+        for (int i = 0; i < C / 4; ++i) {
+          const floatx4 v = reinterpret_cast<const floatx4*>(static_cast<const float*>(p.logits) + first)[i];
 #pragma unroll
-      for (int i = 0; i < C; ++i)
-        if (live[i]) total += expf(l[i] - top);
-      total = wave_sum(total);
-    }
-    // Choice values as keys; `by_score` holds the scores' where groups are summed and no bias is given.
-    int64_t key[C], by_score[C];
-    double total64 = 0.0;
-    if (p.exact_scores && p.score == MOE_SCORE_SOFTMAX) {
-#pragma unroll
-      for (int i = 0; i < C; ++i)
-        if (live[i]) total64 += exp(static_cast<double>(l[i]) - top);
-      total64 = wave_sum64(total64);
-    }
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      key[i] = by_score[i] = kNoKey;
-      if (!live[i]) continue;
-      double s = l[i];
-      if (p.exact_scores)
-        s = p.score == MOE_SCORE_SOFTMAX ? exp(s - top) / total64 : 1.0 / (1.0 + exp(-s));
-      if (p.bias != nullptr) {
-        const float b = p.bias[first + i];
-        if (b == -INFINITY) continue;
-        key[i] = by_score[i] = key_of(s + b);
+          for (int q = 0; q < 4; ++q) l[4 * i + q] = v[q];
+        }
       } else {
-        key[i] = key_of(static_cast<double>(l[i]));
-        by_score[i] = key_of(s);
+#pragma unroll
+        for (int i = 0; i < C / 8; ++i) {
+          const u32x4 v = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.logits) + first)[i];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            l[8 * i + 2 * q] = p.dtype == MOE_DTYPE_BF16 ? bf16_lo(v[q]) : half_bits_to_float(v[q] & 0xFFFF);
+            l[8 * i + 2 * q + 1] = p.dtype == MOE_DTYPE_BF16 ? bf16_hi(v[q]) : half_bits_to_float(v[q] >> 16);
+          }
+        }
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        l[i] = here && d.first + i < d.end ? load_elem(p.logits, at + d.first + i, p.dtype) : -INFINITY;
     }
-    if (p.topk_groups < p.groups) {
-      int64_t a = kNoKey, b = kNoKey;       // the two largest of the group
+    // The softmax's largest logit and its sum, where something needs them.
+    float top = 0.0f, total = 1.0f;
+    if (p.score == MOE_SCORE_SOFTMAX && (kBias || !p.renormalize)) {
+      top = l[0];
+#pragma unroll
+      for (int i = 1; i < C; ++i) top = fmaxf(top, l[i]);
+      top = row_max(top);
+      total = 0.0f;
+#pragma unroll
+      for (int i = 0; i < C; ++i) total += l[i] == -INFINITY ? 0.0f : fast_exp(l[i] - top);
+      total = row_sum(total);
+    }
+    V v[C];
+    if constexpr (kBias) {
+      const float inv = __builtin_amdgcn_rcpf(total);
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        b = max(b, min(a, by_score[i]));
-        a = max(a, by_score[i]);
+        const float b = d.first + i < d.end ? p.bias[d.first + i] : -INFINITY;
+        const float s = p.score == MOE_SCORE_SOFTMAX ? fast_exp(l[i] - top) * inv
+                                                     : __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[i]));
+        const float c = s + b;
+        v[i] = l[i] == -INFINITY || b == -INFINITY ? -INFINITY : c != c ? INFINITY : c;
       }
-      for (int off = 1; off < p.per_group; off <<= 1) {
-        const int64_t oa = __shfl_xor(a, off, kWave), ob = __shfl_xor(b, off, kWave);
-        b = max(min(a, oa), max(b, ob));
-        a = max(a, oa);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] = key32(l[i]);
+    }
+    V a = v[0], b = none<V>();
+#pragma unroll
+    for (int i = 1; i < C; ++i) {
+      b = max(b, min(a, v[i]));
+      a = max(a, v[i]);
+    }
+    bool open = false;                       // the row goes to route_exact
+    if (p.topk_groups < p.groups) {
+      V ga = a, gb = b;
+      const auto merge = [&](V oa, V ob) {
+        gb = max(min(ga, oa), max(gb, ob));
+        ga = max(ga, oa);
+      };
+      if (p.narrow.per_group > 1) merge(partner<1>(ga), partner<1>(gb));
+      if (p.narrow.per_group > 2) merge(partner<2>(ga), partner<2>(gb));
+      if (p.narrow.per_group > 4) merge(partner<4>(ga), partner<4>(gb));
+      V g = ga;
+      float close = 0.0f;                    // ranks this near to each other decide nothing
+      if constexpr (kBias) {
+        const bool two = p.group_top == 2 && gb != -INFINITY;
+        if (two) g = ga + gb;
+        const float size = (ga == -INFINITY ? 0.0f : fabsf(ga)) + (two ? fabsf(gb) : 0.0f);
+        close = 4.0f * err + row_max(size) * 0x1p-21f;
       }
-      int64_t g = a;
-      if (p.group_top == 2 && a != kNanKey && b != kNoKey) g = key_of(value_of(a) + value_of(b));
+      mem.top[lane] = g;
+      wave_lds_fence();
       int rank = 0;
       for (int o = 0; o < p.groups; ++o) {
-        const int64_t og = __shfl(g, o * p.per_group, kWave);
-        rank += (og > g || (og == g && o < group)) ? 1 : 0;
+        const V og = mem.top[o * p.narrow.per_group];
+        rank += (og > g || (og == g && o < d.group)) ? 1 : 0;
+        if constexpr (kBias) open |= o != d.group && fabsf(og - g) <= close;
       }
+      if constexpr (kBias) open = (open || g == INFINITY) && g != -INFINITY;
       if (rank >= p.topk_groups) {
+        a = b = none<V>();
 #pragma unroll
-        for (int i = 0; i < C; ++i) key[i] = kNoKey;
+        for (int i = 0; i < C; ++i) v[i] = none<V>();
       }
+      wave_lds_fence();
     }
-    int mine = -1;                          // expert of slot `lane`
-    for (int j = 0; j < p.k; ++j) {
-      int64_t best = kNoKey;
-      int e = INT32_MAX;
+    mem.top[lane] = a;
+    mem.top[kLanes + lane] = b;
+    wave_lds_fence();
+    int na = 0, nb = 0;
 #pragma unroll
-      for (int i = 0; i < C; ++i)
-        if (key[i] > best) {
-          best = key[i];
-          e = first + i;
-        }
-#pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) {
-        const int64_t ob = __shfl_xor(best, off, kWave);
-        const int oe = __shfl_xor(e, off, kWave);
-        if (ob > best || (ob == best && oe < e)) {
-          best = ob;
-          e = oe;
-        }
-      }
-      if (best == kNoKey) break;
-      if (lane == j) mine = e;
-#pragma unroll
-      for (int i = 0; i < C; ++i)
-        if (first + i == e) key[i] = kNoKey;
+    for (int o = 0; o < 2 * kLanes; ++o) {
+      const V t = mem.top[o];
+      na += t >= a ? 1 : 0;
+      nb += t >= b ? 1 : 0;
     }
-    float s = 0.0f;
-    const float chosen = mine >= 0 ? load_elem(p.logits, at + mine, p.dtype) : -INFINITY;
-    if (p.renormalize) {
-      // Relative to the largest chosen score, so that small scores do not vanish.
-      float m = wave_max(chosen);
-      if (p.score == MOE_SCORE_SOFTMAX) {
-        s = mine >= 0 ? expf(chosen - m) : 0.0f;
-      } else {
-        m = fminf(m, 0.0f);
-        s = mine >= 0 ? expf(fminf(chosen, 0.0f) - m) / (1.0f + expf(-fabsf(chosen))) : 0.0f;
-      }
-      s /= wave_sum(s);
-    } else if (p.score == MOE_SCORE_SOFTMAX) {
-      s = expf(chosen - top) / total;
+    const V bound = row_max(max(na >= p.k ? a : none<V>(), nb >= p.k ? b : none<V>()));
+    uint32_t left = 0;                       // places that stay
+    if constexpr (kBias) {
+      const float low = bound == INFINITY ? bound : bound - (2.0f * err + fabsf(bound) * 0x1p-21f);
+#pragma unroll
+      for (int i = 0; i < C; ++i) left |= (v[i] >= low && v[i] != -INFINITY) ? 1u << i : 0u;
     } else {
-      s = 1.0f / (1.0f + expf(-chosen));
+      // Equal keys are equal values: the first k of those at the bound are enough.
+      uint32_t same = 0;
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        left |= v[i] > bound ? 1u << i : 0u;
+        same |= v[i] == bound && v[i] != INT32_MIN ? 1u << i : 0u;
+      }
+      int room = p.k - row_before(__popc(same));
+      for (; room > 0 && same != 0; --room) {
+        left |= same & -same;
+        same &= same - 1;
+      }
     }
-    if (lane < p.k) {
-      p.topk_ids[row * p.k + lane] = mine;
-      p.topk_w[row * p.k + lane] = mine >= 0 ? p.scale * s : 0.0f;
+    const int count = __popc(left);
+    int slot = row_before(count);
+    const int all = row_sum(count);
+    open = row_max(open || all > kLanes ? 1 : 0) != 0;
+    if (!open) {
+      while (left != 0) {
+        mem.id[slot++] = d.first + __ffs(left) - 1;
+        left &= left - 1;
+      }
     }
+    wave_lds_fence();
+    int id = lane < all && !open ? mem.id[lane] : -1;
+    float chosen = id >= 0 ? load_elem(p.logits, at + id, p.dtype) : -INFINITY;
+    int64_t key = kNoKey;
+    if (id >= 0) {
+      double c = chosen;
+      if constexpr (kBias)
+        c = (p.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-c)) : exp(c - top) / total) + p.bias[id];
+      key = key_of(c);
+    }
+    mem.key[lane] = key;
+    wave_lds_fence();
+    int rank = 0;
+#pragma unroll
+    for (int o = 0; o < kLanes; ++o) {
+      const int64_t t = mem.key[o];
+      rank += (t > key || (t == key && o < lane)) ? 1 : 0;
+      // The softmax's sum is an fp32 one: values as near as its error are not told apart by it.
+      if constexpr (kBias) {
+        if (p.score == MOE_SCORE_SOFTMAX && o != lane && t != kNoKey && key != kNoKey)
+          open |= !(fabs(value_of(t) - value_of(key)) > 2.0 * err);
+      }
+    }
+    if constexpr (kBias) {
+      if (p.score == MOE_SCORE_SOFTMAX) open = row_max(open ? 1 : 0) != 0;
+    }
+    wave_lds_fence();
+    if (id >= 0 && rank < p.k) {
+      mem.id[rank] = id;
+      mem.logit[rank] = chosen;
+    }
+    wave_lds_fence();
+    id = lane < min(all, p.k) ? mem.id[lane] : -1;
+    chosen = id >= 0 ? mem.logit[lane] : -INFINITY;
+    const float s = weight_of(p, id, chosen, top, total, [](float x) { return row_max(x); },
+                              [](float x) { return row_sum(x); });
+    if (here && !open && lane < p.k) {
+      p.topk_ids[row * p.k + lane] = id;
+      p.topk_w[row * p.k + lane] = id >= 0 ? p.scale * s : 0.0f;
+    }
+    uint64_t rest = __ballot(here && open);
+    while (rest != 0) {
+      const int first = __ffsll(static_cast<unsigned long long>(rest)) - 1;
+      route_exact(p, row0 + (threadIdx.x / kWave) * (kWave / kLanes) + first / kLanes,
+                  keys + threadIdx.x / kWave * p.E);
+      rest &= ~(uint64_t(0xFFFF) << (first / kLanes * kLanes));
+    }
+    wave_lds_fence();
   }
 }
 
@@ -256,18 +556,42 @@ __global__ __launch_bounds__(kThreads) void route_grad(RouteGradArgs p) {
       }
       buf[e] = v;
     }
-    // The lanes of a wave exchange through LDS without a barrier: its accesses stay in order.
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_fence();
     const float before = valid ? buf[id] : 0.0f;
     __builtin_amdgcn_wave_barrier();
     if (valid) buf[id] = before + sum;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_fence();
     for (int e = lane; e < p.E; e += kWave) store_elem(p.dlogits, row * p.ldd + e, p.out_dtype, buf[e]);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_fence();
   }
+}
+
+}  // namespace
+
+namespace {
+
+RouteLayout layout(int lanes, int groups, int group_size) {
+  RouteLayout y{1, 0};
+  while (y.per_group * 2 * groups <= lanes) y.per_group *= 2;
+  y.per_lane = (group_size + y.per_group - 1) / y.per_group;
+  return y;
+}
+
+// LDS of route_exact's keys for every wave of a workgroup.
+uint32_t exact_bytes(const RouteArgs& p) { return sizeof(int64_t) * kWaves * p.E; }
+
+template <int C>
+void start_narrow(RouteArgs p, hipStream_t stream) {
+  // Whole 16-byte pieces for every lane of every row.
+  const int64_t bytes = p.dtype == MOE_DTYPE_F32 ? 4 : 2;
+  p.vector = p.groups * p.narrow.per_group == kLanes && p.narrow.per_lane == C &&
+             p.group_size == p.narrow.per_group * C && C * bytes % 16 == 0 && p.ld * bytes % 16 == 0 &&
+             reinterpret_cast<uintptr_t>(p.logits) % 16 == 0;
+  const dim3 grid(grid_for((p.M + kRows - 1) / kRows, 0)), block(kThreads);
+  if (p.bias != nullptr)
+    launch(route_narrow<C, true>, grid, block, exact_bytes(p), stream, p);
+  else
+    launch(route_narrow<C, false>, grid, block, exact_bytes(p), stream, p);
 }
 
 }  // namespace
@@ -275,20 +599,26 @@ __global__ __launch_bounds__(kThreads) void route_grad(RouteGradArgs p) {
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
   RouteArgs p = a;
   p.group_size = p.E / p.groups;
-  p.per_group = 1;
-  while (p.per_group * 2 * p.groups <= kWave) p.per_group *= 2;
-  p.per_lane = (p.group_size + p.per_group - 1) / p.per_group;
+  p.wide = layout(kWave, p.groups, p.group_size);
   // Scores are needed for the choice with a bias, and where they are summed over a group.
-  p.exact_scores = p.bias != nullptr || (p.topk_groups < p.groups && p.group_top == 2);
+  const bool sums = p.topk_groups < p.groups && p.group_top == 2;
+  p.exact_scores = p.bias != nullptr || sums;
+  if (p.groups <= kLanes && p.k <= kLanes && (p.bias != nullptr || !sums)) {
+    p.narrow = layout(kLanes, p.groups, p.group_size);
+    if (p.narrow.per_lane <= 32) {
+      if (p.narrow.per_lane <= 4)
+        start_narrow<4>(p, stream);
+      else if (p.narrow.per_lane <= 8)
+        start_narrow<8>(p, stream);
+      else if (p.narrow.per_lane <= 16)
+        start_narrow<16>(p, stream);
+      else
+        start_narrow<32>(p, stream);
+      return hipGetLastError();
+    }
+  }
   const dim3 grid(grid_for((p.M + kWaves - 1) / kWaves, 0)), block(kThreads);
-  if (p.per_lane <= 2)
-    launch(route<2>, grid, block, 0, stream, p);
-  else if (p.per_lane <= 8)
-    launch(route<8>, grid, block, 0, stream, p);
-  else if (p.per_lane <= 32)
-    launch(route<32>, grid, block, 0, stream, p);
-  else
-    launch(route<64>, grid, block, 0, stream, p);
+  launch(route_wide, grid, block, exact_bytes(p), stream, p);
   return hipGetLastError();
 }
 

@@ -187,7 +187,8 @@ struct MatvecArgs {
   void* y;
   moe_weights w;
   int64_t ldx, ldy, rows;
-  int64_t tasks;             // set by launch_matvec
+  int64_t tasks;             // set by launch_matvec, as the next
+  uint32_t group_inverse;    // 2^31 / (group / 32), rounded up
   int per, E, N, K, group, out_dtype;
 };
 hipError_t launch_matvec(const MatvecArgs& p, int dtype, hipStream_t stream);

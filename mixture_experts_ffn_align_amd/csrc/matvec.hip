@@ -2,12 +2,20 @@
 //   y[r][n] = sum_k (q[e][n][k] - z[e][n][k / g]) s[e][n][k / g] x[r / per][k]
 // with one matrix for every row, or the matrix of the row's expert.
 //
-// The weights are the left operand of 16x16x32 matrix instructions, so up to
-// sixteen rows cost the same unpacking. A nibble is OR-ed into the top of a
-// 16-bit mantissa, which gives 16 + q exactly; a group's sum is then
+// The weights are the right operand of 16x16x32 matrix instructions and x the
+// left one, so up to sixteen rows cost the same unpacking, and a lane's results
+// belong to the weight row that it loads: scale and zero are one value per lane.
+// A nibble is OR-ed into the top of a 16-bit mantissa, which gives 16 + q exactly;
+// a group's sum is then
 //   s (sum (16 + q) x - (16 + z) sum x)
-// in fp32, where sum x comes from a second matrix instruction with ones. (An
-// offset of 128, from the mantissa's low bits, would cancel eight times as much.)
+// in fp32, where sum x comes from a matrix instruction with ones. (An offset of
+// 128, from the mantissa's low bits, would cancel eight times as much.)
+//
+// A wave's loads take whole lines (eight lanes to 128 bytes of a weight row) and
+// pass through LDS into the operands' layout; a load with neighbouring lanes in
+// different rows costs the cache four times as much. Loads go through buffer
+// descriptors, whose bounds give zeros past the ends of rows, features and the
+// wave's share of the summed index.
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -15,10 +23,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kSplit = kThreads / kWave;   // waves that share a tile's summed index
-constexpr int kTile = 16;                  // weight rows of a tile
-constexpr int kChunk = 128;                // summed elements per 16-byte load of a lane
+constexpr int kMaxWaves = 8;   // of a workgroup: they share the summed index
+constexpr int kTile = 16;      // weight rows, and rows of x, of a matrix instruction
 
 typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
 typedef _Float16 halfx8v __attribute__((ext_vector_type(8)));
@@ -33,18 +39,21 @@ __device__ __forceinline__ floatx4 mfma(u32x4 a, u32x4 b, floatx4 c) {
                                                    0, 0);
 }
 
+template <bool kHalf>
+constexpr uint32_t kMask = kHalf ? 0x03C003C0u : 0x00780078u;
+
 // Eight 4-bit values of a word as 16 + q, in element order.
 template <bool kHalf>
-__device__ __forceinline__ u32x4 unpack8(uint32_t w) {
+__device__ __forceinline__ u32x4 unpack8(uint32_t w, uint32_t m) {   // m: kMask in a VGPR (see in_vgpr)
   u32x4 v;
   if constexpr (kHalf) {
-    const uint32_t m = 0x03C003C0u, c = 0x4C004C00u;
+    const uint32_t c = 0x4C004C00u;
     v[0] = ((w << 6) & m) | c;
     v[1] = ((w << 2) & m) | c;
     v[2] = ((w >> 2) & m) | c;
     v[3] = ((w >> 6) & m) | c;
   } else {
-    const uint32_t m = 0x00780078u, c = 0x41804180u;
+    const uint32_t c = 0x41804180u;
     v[0] = ((w << 3) & m) | c;
     v[1] = ((w >> 1) & m) | c;
     v[2] = ((w >> 5) & m) | c;
@@ -64,84 +73,219 @@ __device__ __forceinline__ u32x4 transpose4(u32x4 v) {
                static_cast<uint32_t>(d[1])};
 }
 
-// A workgroup takes sixteen weight rows and up to 16 kCols rows of x; its waves
-// take quarters of the summed index, whose sums meet in LDS.
-template <bool kHalf, int kCols>
-__global__ __launch_bounds__(kThreads) void matvec(MatvecArgs p) {
-  __shared__ floatx4 part[kSplit - 1][kCols][kWave];
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
+  // Wave-uniform, which the compiler has to see: it loops over a descriptor that it takes for a lane's own.
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  const uint32_t lo = uniform(static_cast<int>(a)), hi = uniform(static_cast<int>(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uintptr_t(hi) << 32 | lo), 0,
+                                           uniform(static_cast<int>(bytes)), 0x00020000);
+}
+
+constexpr uint32_t kOutside = 0x80000000u;   // an offset past every buffer here
+
+// A workgroup takes 16 kShare weight rows, 16 to a wave, and up to kRows rows of
+// x; the groups of kShare waves share the summed index, their sums meet in LDS. A
+// step takes kChunk elements of it, whose x a group's waves bring in together.
+// kFlush: products of 32 elements after which a sum is scaled (what divides the
+// group and 128 alike).
+template <bool kHalf, int kChunk, int kRows, int kShare, int kFlush>
+__global__ __launch_bounds__(kMaxWaves* kWave) void matvec(MatvecArgs p) {
+  constexpr int kCols = (kRows + kTile - 1) / kTile;
+  constexpr int kSteps = kChunk / 32;                // products of a chunk
+  constexpr int kWPieces = kSteps, kXPieces = kChunk / 8;   // 16-byte pieces of a chunk of a row
+  constexpr int kWLoads = kTile * kWPieces / kWave;
+  constexpr int kXLoads = kRows * kXPieces / kWave / kShare;
+  constexpr int kSLoads = kTile * kSteps / kWave;
+  // Chunks whose loads are in flight. Loads return in order, so x is as far ahead as the weights.
+  constexpr int kAhead = kXLoads * kChunk <= 512 ? 4 : 2;
+  constexpr int kUnroll = 4;                         // chunks of a batch of scales (kFlush), at most
+  constexpr int kBatches = kAhead > kFlush ? kAhead / kFlush : 1;   // of scales in flight
+  struct Stage {
+    u32x4 w[kTile][kWPieces];
+  };
+  struct Mine {
+    Stage stage[2];
+    uint32_t sz[kTile][kSteps];                      // scale, and zero in the third byte, of kSteps flushes
+  };
+  struct Group {
+    u32x4 x[2][kRows][kXPieces];
+  };
+  extern __shared__ u32x4 lds[];
   const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
-  const int r = lane & 15, q = lane >> 4;
-  const int tiles = (p.N + kTile - 1) / kTile;
+  const int splits = blockDim.x / (kWave * kShare);
+  const int split = wave / kShare, part_of = wave % kShare;
+  Mine& mine = reinterpret_cast<Mine*>(lds)[wave];
+  Group& shared = reinterpret_cast<Group*>(reinterpret_cast<Mine*>(lds) + splits * kShare)[split];
+  const int r = lane & 15, q = lane >> 4;            // in operands: row, eight elements of a product's 32
+  const int lr = lane / kWPieces, lp = lane % kWPieces;     // in loads of weights and scales
+  const int tiles = (p.N + kTile * kShare - 1) / (kTile * kShare);
   const int chunks = (p.K + kChunk - 1) / kChunk;
-  const int c0 = static_cast<int>(int64_t(chunks) * wave / kSplit);
-  const int c1 = static_cast<int>(int64_t(chunks) * (wave + 1) / kSplit);
-  const int words = p.K / 8, groups = p.K / p.group;
+  const int per = (chunks + splits - 1) / splits;
+  const int c0 = per * split, c1 = min(c0 + per, chunks);
+  const int groups = p.K / p.group;
   const uint32_t one = kHalf ? 0x3C003C00u : 0x3F803F80u;
   const u32x4 ones = {one, one, one, one};
+  const uint32_t mask = in_vgpr(kMask<kHalf>);
   for (int64_t task = blockIdx.x; task < p.tasks; task += gridDim.x) {
-    const int64_t block = task / tiles;
-    const int n0 = static_cast<int>(task - block * tiles) * kTile;
-    const int64_t row0 = p.ids != nullptr ? block : block * (kTile * kCols);
-    const int rows = p.ids != nullptr ? 1 : static_cast<int>(min(int64_t(kTile * kCols), p.rows - row0));
-    const int e = p.ids != nullptr ? p.ids[row0] : 0;
+    // (64-bit divisions are vector code: `uniform` keeps the descriptors scalar.)
+    const int block = uniform(static_cast<int>(task / tiles));
+    const int n0 = uniform(static_cast<int>(task - int64_t(block) * tiles)) * (kTile * kShare) + part_of * kTile;
+    const int64_t row0 = p.ids != nullptr ? block : int64_t(block) * kRows;
+    const int rows = p.ids != nullptr ? 1 : static_cast<int>(min(int64_t(kRows), p.rows - row0));
+    const int e = p.ids != nullptr ? uniform(p.ids[row0]) : 0;
     floatx4 acc[kCols] = {};
     if (e >= 0 && e < p.E) {
-      const int64_t wrow = int64_t(e) * p.N + min(n0 + r, p.N - 1);
-      const uint32_t* w = static_cast<const uint32_t*>(p.w.q) + wrow * words;
-      const uint16_t* x[kCols];
+      const int have = max(0, min(kTile, p.N - n0));
+      const int64_t w0 = int64_t(e) * p.N + (have > 0 ? n0 : 0);
+      const auto wbuf = buffer_of(static_cast<const uint8_t*>(p.w.q) + w0 * (p.K / 2), int64_t(have) * (p.K / 2));
+      const auto sbuf = buffer_of(static_cast<const uint16_t*>(p.w.scale) + w0 * groups, int64_t(have) * groups * 2);
+      const auto zbuf = buffer_of(p.w.zero != nullptr ? p.w.zero + w0 * groups : static_cast<const uint8_t*>(p.w.q),
+                                  p.w.zero != nullptr ? int64_t(have) * groups : 0);
+      const auto xbuf = buffer_of(static_cast<const uint16_t*>(p.x) + uniform(static_cast<int>(row0 / p.per)) * p.ldx,
+                                  (int64_t(rows - 1) * p.ldx + p.K) * 2);
+      const float zbase = p.w.zero != nullptr ? 16.0f : 24.0f;
+      u32x4 w[kAhead][kWLoads], x[kAhead][kXLoads];
+      const int xp = lane % kXPieces;                  // in loads of x
+      const auto xrow = [&](int i) { return (i * kShare + part_of) * (kWave / kXPieces) + lane / kXPieces; };
+      const auto load = [&](int c, u32x4* wr, u32x4* xr) {
+        const uint32_t at = c < c1 ? c * (kChunk / 2) : kOutside;
 #pragma unroll
-      for (int c = 0; c < kCols; ++c)
-        x[c] = static_cast<const uint16_t*>(p.x) + (row0 + min(c * kTile + r, rows - 1)) / p.per * p.ldx + q * 8;
-      int64_t srow[4];
+        for (int i = 0; i < kWLoads; ++i)
+          wr[i] = __builtin_amdgcn_raw_buffer_load_b128(
+              wbuf, uint32_t(i * (kWave / kWPieces) + lr) * (p.K / 2) + lp * 16 + at, 0, 0);
+        // Past the sum's end x has to be zero; the weights there are another row's, and finite.
+        const int left = c < c1 ? (p.K - c * kChunk) / 8 : 0;
+        const uint32_t xat = xp < left ? c * (kChunk * 2) + xp * 16 : kOutside;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) srow[i] = (int64_t(e) * p.N + min(n0 + q * 4 + i, p.N - 1)) * groups;
-      for (int c = c0; c < c1; ++c) {
-        const int word = c * (kChunk / 8) + q * 4;
-        u32x4 v = {0, 0, 0, 0};
-        if (word < words) v = *reinterpret_cast<const u32x4*>(w + word);
-        v = transpose4(v);
-        const int steps = min(4, (p.K - c * kChunk) / 32);
-        floatx4 sum[kCols] = {}, xs[kCols] = {};
-        for (int j = 0; j < steps; ++j) {
-          const int k = c * kChunk + j * 32;
-          const u32x4 a = unpack8<kHalf>(j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3]);
+        for (int i = 0; i < kXLoads; ++i)
+          xr[i] = __builtin_amdgcn_raw_buffer_load_b128(
+              xbuf, uint32_t(xrow(i)) * static_cast<uint32_t>(p.ldx) * 2 + xat, 0, 0);
+      };
+      const auto load_sz = [&](int c, uint16_t* sc, uint8_t* ze) {   // kSteps flushes from chunk c on
+        const int g = min(static_cast<int>(__umulhi(2 * (c * kSteps + lp * kFlush), p.group_inverse)), groups - 1);
 #pragma unroll
-          for (int m = 0; m < kCols; ++m) {
-            const u32x4 b = *reinterpret_cast<const u32x4*>(x[m] + k);
-            sum[m] = mfma<kHalf>(a, b, sum[m]);
-            xs[m] = mfma<kHalf>(ones, b, xs[m]);
-          }
-          if (j == steps - 1 || (k + 32) % p.group == 0) {
-            const int g = k / p.group;
+        for (int i = 0; i < kSLoads; ++i) {
+          const uint32_t at = uint32_t(i * (kWave / kWPieces) + lr) * groups + g;
+          sc[i] = __builtin_amdgcn_raw_buffer_load_b16(sbuf, at * 2, 0, 0);
+          ze[i] = __builtin_amdgcn_raw_buffer_load_b8(zbuf, at, 0, 0);
+        }
+      };
+      // Pieces lie at an exclusive or with their row's number, so that eight rows' same piece is in other banks.
+      constexpr int kTurn = kWPieces == 8 ? 1 : 2;
+      const auto store = [&](int b, const u32x4* wr, const u32x4* xr) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float s = half_bits_to_float(static_cast<const uint16_t*>(p.w.scale)[srow[i] + g]);
-              const float z = 16.0f + (p.w.zero != nullptr ? static_cast<float>(p.w.zero[srow[i] + g]) : 8.0f);
+        for (int i = 0; i < kWLoads; ++i) {
+          const int row = i * (kWave / kWPieces) + lr;
+          mine.stage[b].w[row][lp ^ (row >> kTurn)] = wr[i];
+        }
 #pragma unroll
-              for (int m = 0; m < kCols; ++m) acc[m][i] += s * (sum[m][i] - z * xs[m][i]);
-            }
+        for (int i = 0; i < kXLoads; ++i) shared.x[b][xrow(i)][xp ^ (xrow(i) & 15)] = xr[i];
+      };
+      const auto store_sz = [&](const uint16_t* sc, const uint8_t* ze) {
+#pragma unroll
+        for (int i = 0; i < kSLoads; ++i) {            // (not joined in a register: that would wait for the loads)
+          char* at = reinterpret_cast<char*>(&mine.sz[i * (kWave / kWPieces) + lr][lp]);
+          __builtin_memcpy(at, &sc[i], 2);
+          __builtin_memcpy(at + 2, &ze[i], 1);
+        }
+      };
+      uint32_t szs[kSteps];
+      // A chunk in LDS: u-th of those that share a batch of scales.
+      const auto multiply = [&](int b, int u) {
+        u32x4 v[kWLoads];
+#pragma unroll
+        for (int h = 0; h < kWLoads; ++h) v[h] = transpose4(mine.stage[b].w[r][(h * 4 + q) ^ (r >> kTurn)]);
+        floatx4 sum[kCols], xs[kCols];
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+          if (j % kFlush == 0) {
 #pragma unroll
             for (int m = 0; m < kCols; ++m) sum[m] = xs[m] = floatx4{0, 0, 0, 0};
           }
-        }
-      }
-    }
-    if (wave > 0) {
+          const u32x4 weights = unpack8<kHalf>(v[j / 4][j % 4], mask);
 #pragma unroll
-      for (int m = 0; m < kCols; ++m) part[wave - 1][m][lane] = acc[m];
+          for (int m = 0; m < kCols; ++m) {
+            const int row = (m * kTile + r) % kRows;
+            const u32x4 a = shared.x[b][row][(j * 4 + q) ^ (row & 15)];
+            xs[m] = mfma<kHalf>(a, ones, xs[m]);
+            sum[m] = mfma<kHalf>(a, weights, sum[m]);
+          }
+          if (j % kFlush == kFlush - 1) {
+            const uint32_t h = szs[u * (kSteps / kFlush) + j / kFlush];
+            const float sv = half_bits_to_float(h & 0xFFFF), z = zbase + static_cast<float>(h >> 16 & 0xFF);
+#pragma unroll
+            for (int m = 0; m < kCols; ++m) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[m][i] += sv * (sum[m][i] - z * xs[m][i]);
+            }
+          }
+        }
+      };
+      uint16_t sc[kBatches][kSLoads];
+      uint8_t ze[kBatches][kSLoads];
+      // Step c: chunk c + 1 goes to LDS, chunk c + 1 + kAhead is requested, chunk c is multiplied.
+      const auto step = [&](int c, int u, bool more) {
+        __builtin_amdgcn_sched_barrier(0);   // or later chunks' loads move up and take registers
+        if constexpr (kShare > 1) lds_barrier();
+        if (u % kFlush == 0) {
+#pragma unroll
+          for (int f = 0; f < kSteps; ++f) szs[f] = mine.sz[r][f];
+          const int next = (u / kFlush + 1) % kBatches;
+          store_sz(sc[next], ze[next]);
+          if (more || u + (1 + kBatches) * kFlush < kUnroll)
+            load_sz(c + u + (1 + kBatches) * kFlush, sc[next], ze[next]);
+        }
+        store((u + 1) & 1, w[(u + 1) % kAhead], x[(u + 1) % kAhead]);
+        if (more || u + 1 + kAhead < kUnroll) load(c + u + 1 + kAhead, w[(u + 1) % kAhead], x[(u + 1) % kAhead]);
+        multiply(u & 1, u % kFlush);
+      };
+      // In the loop's order, or the waits at its head would be for these loads' order instead: chunk t is
+      // requested by step t - 1 - kAhead.
+      uint16_t sc0[kSLoads];
+      uint8_t ze0[kSLoads];
+      load_sz(c0, sc0, ze0);
+      if constexpr (kAhead + 1 < kFlush) load_sz(c0 + kFlush, sc[0], ze[0]);
+#pragma unroll
+      for (int t = 0; t <= kAhead; ++t) {
+        __builtin_amdgcn_sched_barrier(0);
+        if ((kAhead + 1 - t) % kFlush == 0) {
+          const int batch = 1 + kBatches - (kAhead + 1 - t) / kFlush;
+          if (batch > 0) load_sz(c0 + batch * kFlush, sc[batch % kBatches], ze[batch % kBatches]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (t == kAhead) {
+          store_sz(sc0, ze0);
+          store(0, w[0], x[0]);
+        }
+        load(c0 + t, w[t % kAhead], x[t % kAhead]);
+      }
+      // Waves that meet at barriers take as many chunks; those past the sum's end are zeros.
+      const int end = kShare > 1 ? c0 + per : c1;
+      int c = c0;
+      for (; c + kUnroll <= end; c += kUnroll) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) step(c, u, true);
+      }
+      if (c < end) step(c, 0, false);
+      if (c + 1 < end) step(c, 1, false);
+      if (c + 2 < end) step(c, 2, false);
     }
     __syncthreads();
-    if (wave == 0) {
+    floatx4* part = reinterpret_cast<floatx4*>(lds);
+    if (split > 0) {
+#pragma unroll
+      for (int m = 0; m < kCols; ++m) part[((wave - kShare) * kCols + m) * kWave + lane] = acc[m];
+    }
+    __syncthreads();
+    if (split == 0) {
+      const int n = n0 + r;
 #pragma unroll
       for (int m = 0; m < kCols; ++m) {
-#pragma unroll
-        for (int s = 0; s < kSplit - 1; ++s) acc[m] += part[s][m][lane];
-        const int col = m * kTile + r;
-        if (col >= rows) continue;
+        for (int s = 1; s < splits; ++s) acc[m] += part[((wave + (s - 1) * kShare) * kCols + m) * kWave + lane];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int n = n0 + q * 4 + i;
-          if (n >= p.N) continue;
+          const int col = m * kTile + q * 4 + i;
+          if (col >= rows || n >= p.N) continue;
           const int64_t at = (row0 + col) * p.ldy + n;
           if (p.out_dtype == MOE_DTYPE_F32)
             static_cast<float*>(p.y)[at] = acc[m][i];
@@ -156,27 +300,76 @@ __global__ __launch_bounds__(kThreads) void matvec(MatvecArgs p) {
   }
 }
 
-template <int kCols>
-void start(MatvecArgs p, int dtype, hipStream_t stream) {
-  const int64_t tiles = (p.N + kTile - 1) / kTile;
-  const int64_t blocks = p.ids != nullptr ? p.rows : (p.rows + kTile * kCols - 1) / (kTile * kCols);
+template <bool kHalf, int kChunk, int kRows, int kShare>
+void start(MatvecArgs p, int splits, hipStream_t stream) {
+  const int64_t tiles = (p.N + kTile * kShare - 1) / (kTile * kShare);
+  const int64_t blocks = p.ids != nullptr ? p.rows : (p.rows + kRows - 1) / kRows;
   p.tasks = tiles * blocks;
-  const dim3 grid(grid_for(p.tasks, 0)), block(kThreads);
-  if (dtype == MOE_DTYPE_F16)
-    launch(matvec<true, kCols>, grid, block, 0, stream, p);
+  // Products of 32 elements to their group: exact for the 2^15 + 2^7 that are asked for at most.
+  p.group_inverse = static_cast<uint32_t>(((uint64_t(1) << 31) + p.group / 32 - 1) / (p.group / 32));
+  const int waves = splits * kShare;
+  const dim3 grid(grid_for(p.tasks, 0)), block(waves * kWave);
+  uint32_t lds = waves * (2 * kTile * kChunk / 2 + kTile * kChunk / 8) + splits * 2 * kRows * kChunk * 2;
+  const uint32_t sums = (splits - 1) * kShare * ((kRows + kTile - 1) / kTile) * kWave * 16;
+  lds = lds > sums ? lds : sums;
+  if (p.group % 128 == 0)
+    launch(matvec<kHalf, kChunk, kRows, kShare, 4>, grid, block, lds, stream, p);
+  else if (p.group % 64 == 0)
+    launch(matvec<kHalf, kChunk, kRows, kShare, 2>, grid, block, lds, stream, p);
   else
-    launch(matvec<false, kCols>, grid, block, 0, stream, p);
+    launch(matvec<kHalf, kChunk, kRows, kShare, 1>, grid, block, lds, stream, p);
+}
+
+// Few workgroups share the summed index among more waves, many share x among more.
+// Times in us (bf16, groups of 128), N x K, rows, and kShare x splits:
+//   rows <= 4: 512 x 8192, 1 row: 1x8 6.5, 1x4 7.2, 1x2 11.1; 4096 x 2048: 1x4 4.2, 1x8 4.3, 1x2 5.0;
+//     3072 tiles of routed experts, K 2048: 1x2 17.0, 1x4 20.1; 1024 of K 768: 1x2 5.5, 1x4 7.3;
+//     16384 x 8192: chunks of 256, 1x2 18.9, of 128: 1x4 21.0, 1x2 22.3
+//   16 rows: 4096 x 2048: 1x4 5.3, 2x4 6.2, 4x2 7.7; 8192 x 2048: 2x2 6.9, 1x4 7.5, 4x2 8.1;
+//     8192 x 8192: 2x4 14.1, 2x2 15.2, 1x4 15.7; 16384 x 8192: 4x2 21.1, 2x4 29.9, 1x4 33.7
+//   64 rows: 512 x 8192: 2x4 30, 2x2 34, 4x2 43; 8192 x 2048: 2x2 15.5, 2x4 18.1, 4x2 20.8;
+//     16384 x 8192: 4x2 54.5, 4x1 59.9, 2x2 61.5; 200 rows, 8192 x 2048: 4x1 28.7, 2x2 39.3, 4x2 41.7
+template <bool kHalf, int kRows>
+void by_tiles(const MatvecArgs& p, int64_t tiles, hipStream_t stream) {
+  if (tiles < 1024)
+    start<kHalf, 128, kRows, 2>(p, p.K >= 4096 ? 4 : 2, stream);
+  else
+    start<kHalf, 128, kRows, 4>(p, tiles < 2048 ? 2 : 1, stream);
+}
+
+template <bool kHalf>
+void by_shape(const MatvecArgs& p, hipStream_t stream) {
+  const int64_t rows = p.ids != nullptr ? 1 : p.rows;
+  const int64_t tiles = (p.N + kTile - 1) / kTile * (p.ids != nullptr ? p.rows : (p.rows + 4 * kTile - 1) / (4 * kTile));
+  if (rows <= 4) {
+    if (tiles >= 1024 && p.K >= 4096)
+      start<kHalf, 256, 4, 1>(p, 2, stream);
+    else
+      start<kHalf, 128, 4, 1>(p, tiles > 1024 || (tiles >= 1024 && p.K < 1024) ? 2 : tiles <= 256 && p.K >= 4096 ? 8 : 4,
+                              stream);
+  } else if (rows <= kTile) {
+    if (tiles < 512)
+      start<kHalf, 128, 16, 1>(p, 4, stream);
+    else if (tiles < 1024)
+      start<kHalf, 128, 16, 2>(p, p.K >= 8192 ? 4 : 2, stream);
+    else
+      start<kHalf, 128, 16, 4>(p, 2, stream);
+  } else if (rows <= 2 * kTile) {
+    by_tiles<kHalf, 32>(p, tiles, stream);
+  } else if (rows <= 3 * kTile) {
+    by_tiles<kHalf, 48>(p, tiles, stream);
+  } else {
+    by_tiles<kHalf, 64>(p, tiles, stream);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_matvec(const MatvecArgs& p, int dtype, hipStream_t stream) {
-  if (p.ids != nullptr || p.rows <= kTile)
-    start<1>(p, dtype, stream);
-  else if (p.rows <= 2 * kTile)
-    start<2>(p, dtype, stream);
+  if (dtype == MOE_DTYPE_F16)
+    by_shape<true>(p, stream);
   else
-    start<4>(p, dtype, stream);
+    by_shape<false>(p, stream);
   return hipGetLastError();
 }
 

@@ -159,6 +159,7 @@ struct RouteGradArgs {
   int E, k, dtype, out_dtype, score;
   bool renormalize;
   float scale;
+  bool vector, vector_out;   // set by launch_route_grad: rows in pieces of four elements
 };
 hipError_t launch_route_grad(const RouteGradArgs& p, hipStream_t stream);
 

@@ -489,79 +489,148 @@ __global__ __launch_bounds__(kThreads) void route_narrow(RouteArgs p) {
   }
 }
 
-// A wave takes a row: lane j holds slot j. With c = scale, p the scores and
+// Lane j of a row holds slot j. With c = scale, p the scores and
 // u = p / sum of the chosen p:
 //   softmax               dl_e = c p_e ([e chosen] g_e - sum_j g_j p_j)
 //   softmax, renormalised dl_j = c u_j (g_j - sum_i g_i u_i), 0 elsewhere
 //   sigmoid               dl_j = c g_j p_j (1 - p_j)
 //   sigmoid, renormalised dl_j = c u_j (1 - p_j) (g_j - sum_i g_i u_i)
 // Slots are separate arguments: an expert named twice gets both slots' shares.
+//
+// kLanes lanes take a row: a wave any row, sixteen lanes rows of up to 16 slots
+// and 512 experts. Slots meet the row in LDS, and the row is written in pieces of
+// four elements. Bound: HBM, by the writes where the row is not read: 32768 rows
+// of 256 fp32, top-8, 10 us.
+template <int kRowLanes>
+struct GradRow;
+
+template <>
+struct GradRow<kWave> {
+  static __device__ __forceinline__ float max_of(float v) { return wave_max(v); }
+  static __device__ __forceinline__ float sum_of(float v) { return wave_sum(v); }
+};
+
+template <>
+struct GradRow<kLanes> {
+  static __device__ __forceinline__ float max_of(float v) { return row_max(v); }
+  static __device__ __forceinline__ float sum_of(float v) { return row_sum(v); }
+};
+
+// Four elements from element i on (i a multiple of four), or as many as the row has.
+__device__ __forceinline__ floatx4 load_piece(const void* p, int64_t at, int i, int E, int dtype, bool vector) {
+  floatx4 v;
+  if (!vector) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = i + q < E ? load_elem(p, at + i + q, dtype) : -INFINITY;
+  } else if (dtype == MOE_DTYPE_F32) {
+    v = *reinterpret_cast<const floatx4*>(static_cast<const float*>(p) + at + i);
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at + i);
+    const bool bf = dtype == MOE_DTYPE_BF16;
+    v[0] = bf ? bf16_lo(w.x) : half_bits_to_float(w.x & 0xFFFF);
+    v[1] = bf ? bf16_hi(w.x) : half_bits_to_float(w.x >> 16);
+    v[2] = bf ? bf16_lo(w.y) : half_bits_to_float(w.y & 0xFFFF);
+    v[3] = bf ? bf16_hi(w.y) : half_bits_to_float(w.y >> 16);
+  }
+  return v;
+}
+
+__device__ __forceinline__ void store_piece(void* p, int64_t at, int i, int E, int dtype, bool vector, floatx4 v) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  typedef _Float16 halfx4 __attribute__((ext_vector_type(4)));
+  if (!vector) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (i + q < E) store_elem(p, at + i + q, dtype, v[q]);
+  } else if (dtype == MOE_DTYPE_F32) {
+    *reinterpret_cast<floatx4*>(static_cast<float*>(p) + at + i) = v;
+  } else if (dtype == MOE_DTYPE_BF16) {
+    *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p) + at + i) = __builtin_convertvector(v, bf16x4);
+  } else {
+    *reinterpret_cast<halfx4*>(static_cast<_Float16*>(p) + at + i) = __builtin_convertvector(v, halfx4);
+  }
+}
+
+template <int kRowLanes>
 __global__ __launch_bounds__(kThreads) void route_grad(RouteGradArgs p) {
-  extern __shared__ float rows_lds[];
-  const int lane = threadIdx.x & (kWave - 1);
-  float* buf = rows_lds + (threadIdx.x / kWave) * p.E;
-  for (int64_t row = blockIdx.x * int64_t(kWaves) + threadIdx.x / kWave; row < p.M; row += int64_t(gridDim.x) * kWaves) {
+  extern __shared__ floatx4 rows_lds[];
+  constexpr int kHere = kThreads / kRowLanes;          // rows of a workgroup
+  using Row = GradRow<kRowLanes>;
+  const int lane = threadIdx.x % kRowLanes;
+  const int pieces = (p.E + 3) / 4;
+  floatx4* buf = rows_lds + threadIdx.x / kRowLanes * pieces;
+  float* one = reinterpret_cast<float*>(buf);
+  const bool dense = p.score == MOE_SCORE_SOFTMAX && !p.renormalize;
+  for (int64_t row0 = blockIdx.x * int64_t(kHere); row0 < p.M; row0 += int64_t(gridDim.x) * kHere) {
+    const int64_t row = row0 + threadIdx.x / kRowLanes;
+    const bool here = row < p.M;
     const int64_t at = row * p.ld;
-    int id = lane < p.k ? p.topk_ids[row * p.k + lane] : -1;
+    int id = here && lane < p.k ? p.topk_ids[row * p.k + lane] : -1;
     if (id >= p.E) id = -1;
     const bool valid = id >= 0;
     const float g = valid ? p.scale * p.dtopk_w[row * p.k + lane] : 0.0f;
     const float l = valid ? load_elem(p.logits, at + id, p.dtype) : -INFINITY;
-    float d = 0.0f, back = 0.0f, top = 0.0f, total = 1.0f;
-    const bool dense = p.score == MOE_SCORE_SOFTMAX && !p.renormalize;
-    const bool any = __ballot(valid) != 0;
-    if (dense && any) {
-      top = -INFINITY;
-      for (int e = lane; e < p.E; e += kWave) top = fmaxf(top, load_elem(p.logits, at + e, p.dtype));
-      top = wave_max(top);
-      total = 0.0f;
-      for (int e = lane; e < p.E; e += kWave) {
-        const float v = load_elem(p.logits, at + e, p.dtype);
-        total += v == -INFINITY ? 0.0f : expf(v - top);
+    float d = 0.0f;
+    if (dense) {
+      // The row goes through LDS from here on: logits, then gradients.
+      float top = -INFINITY;
+      for (int i = lane; here && i < pieces; i += kRowLanes) {
+        const floatx4 v = load_piece(p.logits, at, 4 * i, p.E, p.dtype, p.vector);
+        buf[i] = v;
+        top = fmaxf(fmaxf(fmaxf(top, v[0]), v[1]), fmaxf(v[2], v[3]));
       }
-      total = wave_sum(total);
-      const float s = valid ? expf(l - top) / total : 0.0f;
+      top = Row::max_of(top);
+      float total = 0.0f;
+      for (int i = lane; here && i < pieces; i += kRowLanes) {
+        floatx4 v = buf[i];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = v[q] == -INFINITY ? 0.0f : fast_exp(v[q] - top);
+        buf[i] = v;
+        total += (v[0] + v[1]) + (v[2] + v[3]);
+      }
+      total = Row::sum_of(total);
+      const float s = valid ? fast_exp(l - top) / total : 0.0f;
       d = valid ? g * s : 0.0f;
-      back = wave_sum(d);
-    } else if (p.score == MOE_SCORE_SOFTMAX) {
-      const float m = wave_max(l);
-      const float e = valid ? expf(l - m) : 0.0f;
-      const float u = e / wave_sum(e);
-      const float dot = wave_sum(valid ? g * u : 0.0f);
-      d = valid ? u * (g - dot) : 0.0f;
+      // A row without any route has no gradient, whatever its softmax.
+      const bool any = Row::max_of(valid ? 1.0f : 0.0f) != 0.0f;
+      const float back = any ? Row::sum_of(d) / total : 0.0f;
+      for (int i = lane; here && i < pieces; i += kRowLanes) buf[i] = any ? -back * buf[i] : floatx4{0, 0, 0, 0};
     } else {
-      const float q = 1.0f / (1.0f + expf(l));       // 1 - p
-      if (p.renormalize) {
-        const float m = fminf(wave_max(l), 0.0f);
-        const float e = valid ? expf(fminf(l, 0.0f) - m) / (1.0f + expf(-fabsf(l))) : 0.0f;
-        const float u = e / wave_sum(e);
-        const float dot = wave_sum(valid ? g * u : 0.0f);
-        d = valid ? u * q * (g - dot) : 0.0f;
+      for (int i = lane; here && i < pieces; i += kRowLanes) buf[i] = floatx4{0, 0, 0, 0};
+      const float m = Row::max_of(l);
+      if (p.score == MOE_SCORE_SOFTMAX) {
+        const float e = valid ? expf(l - m) : 0.0f;
+        const float u = e / Row::sum_of(e);
+        const float dot = Row::sum_of(valid ? g * u : 0.0f);
+        d = valid ? u * (g - dot) : 0.0f;
       } else {
-        d = valid ? g * q / (1.0f + expf(-l)) : 0.0f;
+        const float q = 1.0f / (1.0f + expf(l));       // 1 - p
+        if (p.renormalize) {
+          const float z = fminf(m, 0.0f);
+          const float e = valid ? expf(fminf(l, 0.0f) - z) / (1.0f + expf(-fabsf(l))) : 0.0f;
+          const float u = e / Row::sum_of(e);
+          const float dot = Row::sum_of(valid ? g * u : 0.0f);
+          d = valid ? u * q * (g - dot) : 0.0f;
+        } else {
+          d = valid ? g * q / (1.0f + expf(-l)) : 0.0f;
+        }
       }
     }
-    // Slots that name the same expert: each takes their sum, in slot order.
+    // Slots that name the same expert: the first of them brings their sum.
     float sum = 0.0f;
+    bool first = valid;
     for (int j = 0; j < p.k; ++j) {
-      const int oid = __shfl(id, j, kWave);
-      const float od = __shfl(d, j, kWave);
-      if (oid == id) sum += od;
-    }
-    for (int e = lane; e < p.E; e += kWave) {
-      float v = 0.0f;
-      if (dense && any) {
-        const float x = load_elem(p.logits, at + e, p.dtype);
-        v = x == -INFINITY ? 0.0f : -expf(x - top) / total * back;
-      }
-      buf[e] = v;
+      const int oid = __shfl(id, j, kRowLanes);
+      const float od = __shfl(d, j, kRowLanes);
+      if (oid != id) continue;
+      sum += od;
+      first = first && j >= lane;
     }
     wave_lds_fence();
-    const float before = valid ? buf[id] : 0.0f;
-    __builtin_amdgcn_wave_barrier();
-    if (valid) buf[id] = before + sum;
+    if (first) one[id] += sum;
     wave_lds_fence();
-    for (int e = lane; e < p.E; e += kWave) store_elem(p.dlogits, row * p.ldd + e, p.out_dtype, buf[e]);
+    for (int i = lane; here && i < pieces; i += kRowLanes)
+      store_piece(p.dlogits, row * p.ldd, 4 * i, p.E, p.out_dtype, p.vector_out, buf[i]);
     wave_lds_fence();
   }
 }
@@ -622,9 +691,23 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_route_grad(const RouteGradArgs& p, hipStream_t stream) {
-  const dim3 grid(grid_for((p.M + kWaves - 1) / kWaves, 0)), block(kThreads);
-  launch(route_grad, grid, block, sizeof(float) * kWaves * p.E, stream, p);
+hipError_t launch_route_grad(const RouteGradArgs& a, hipStream_t stream) {
+  RouteGradArgs p = a;
+  // Pieces of four elements, aligned as such.
+  const auto vector = [&](const void* v, int64_t ld, int dtype) {
+    const uintptr_t bytes = dtype == MOE_DTYPE_F32 ? 16 : 8;
+    return p.E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(v) % bytes == 0;
+  };
+  p.vector = vector(p.logits, p.ld, p.dtype);
+  p.vector_out = vector(p.dlogits, p.ldd, p.out_dtype);
+  const int lanes = p.k <= kLanes && p.E <= 512 ? kLanes : kWave;
+  const int rows = kThreads / lanes;
+  const dim3 grid(grid_for((p.M + rows - 1) / rows, 0)), block(kThreads);
+  const uint32_t lds = sizeof(floatx4) * rows * ((p.E + 3) / 4);
+  if (lanes == kLanes)
+    launch(route_grad<kLanes>, grid, block, lds, stream, p);
+  else
+    launch(route_grad<kWave>, grid, block, lds, stream, p);
   return hipGetLastError();
 }
 

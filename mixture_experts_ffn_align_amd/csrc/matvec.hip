@@ -328,11 +328,12 @@ void start(MatvecArgs p, int splits, hipStream_t stream) {
 //   16 rows: 4096 x 2048: 1x4 5.3, 2x4 6.2, 4x2 7.7; 8192 x 2048: 2x2 6.9, 1x4 7.5, 4x2 8.1;
 //     8192 x 8192: 2x4 14.1, 2x2 15.2, 1x4 15.7; 16384 x 8192: 4x2 21.1, 2x4 29.9, 1x4 33.7
 //   64 rows: 512 x 8192: 2x4 30, 2x2 34, 4x2 43; 8192 x 2048: 2x2 15.5, 2x4 18.1, 4x2 20.8;
-//     16384 x 8192: 4x2 54.5, 4x1 59.9, 2x2 61.5; 200 rows, 8192 x 2048: 4x1 28.7, 2x2 39.3, 4x2 41.7
+//     16384 x 8192: 4x2 54.5, 4x1 59.9, 2x2 61.5; 200 rows, 8192 x 2048: 4x1 28.7, 2x2 39.3, 4x2 41.7;
+//     37 rows, 5001 x 4064, groups of 32: 2x4 16.7, 2x2 18.2, 4x2 24.3
 template <bool kHalf, int kRows>
 void by_tiles(const MatvecArgs& p, int64_t tiles, hipStream_t stream) {
   if (tiles < 1024)
-    start<kHalf, 128, kRows, 2>(p, p.K >= 4096 ? 4 : 2, stream);
+    start<kHalf, 128, kRows, 2>(p, p.K > 2048 ? 4 : 2, stream);
   else
     start<kHalf, 128, kRows, 4>(p, tiles < 2048 ? 2 : 1, stream);
 }

@@ -105,6 +105,26 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// A value of another of sixteen neighbouring lanes (rotated by kBy).
+template <int kBy>
+__device__ __forceinline__ float ror(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 | kBy, 0xF, 0xF, false));
+}
+template <int kBy>
+__device__ __forceinline__ int ror(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, 0x120 | kBy, 0xF, 0xF, false);
+}
+
+template <int kBy>
+__device__ __forceinline__ int64_t ror(int64_t v) {
+  const uint32_t lo = ror<kBy>(static_cast<int>(v)), hi = ror<kBy>(static_cast<int>(v >> 32));
+  return static_cast<int64_t>(uint64_t(hi) << 32 | lo);
+}
+template <int kBy>
+__device__ __forceinline__ double ror(double v) {
+  return __longlong_as_double(ror<kBy>(static_cast<int64_t>(__double_as_longlong(v))));
+}
+
 // One row by a whole wave, every choice value in 64 bits and kept in LDS (E
 // keys): any sizes, and the rows that `route_narrow` cannot decide.
 __device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t row, int64_t* key) {
@@ -171,15 +191,18 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t row, int
         e = i;
       }
     }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const int64_t ob = __shfl_xor(best, off, kWave);
-      const int oe = __shfl_xor(e, off, kWave);
+    const auto take = [&](int64_t ob, int oe) {
       if (ob > best || (ob == best && oe < e)) {
         best = ob;
         e = oe;
       }
-    }
+    };
+    take(ror<8>(best), ror<8>(e));
+    take(ror<4>(best), ror<4>(e));
+    take(ror<2>(best), ror<2>(e));
+    take(ror<1>(best), ror<1>(e));
+    take(__shfl_xor(best, 16, kWave), __shfl_xor(e, 16, kWave));
+    take(__shfl_xor(best, 32, kWave), __shfl_xor(e, 32, kWave));
     if (best == kNoKey) break;
     if (lane == j) mine = e;
     if (lane == 0) key[e] = kNoKey;
@@ -203,16 +226,6 @@ __global__ __launch_bounds__(kThreads) void route_wide(RouteArgs p) {
 
 constexpr int kLanes = 16;                 // of a row in route_narrow
 constexpr int kRows = kThreads / kLanes;
-
-// A value of another of the row's sixteen lanes (rotated by kBy).
-template <int kBy>
-__device__ __forceinline__ float ror(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 | kBy, 0xF, 0xF, false));
-}
-template <int kBy>
-__device__ __forceinline__ int ror(int v) {
-  return __builtin_amdgcn_update_dpp(0, v, 0x120 | kBy, 0xF, 0xF, false);
-}
 
 // Reductions over a row's sixteen lanes; every lane ends with the same bits.
 template <typename V>
@@ -254,6 +267,13 @@ __device__ __forceinline__ int key32(float v) {
   return b ^ ((b >> 31) & INT32_MAX);
 }
 
+template <int kStep>
+__device__ __forceinline__ double partner(double v) {
+  const int64_t b = __double_as_longlong(v);
+  const uint32_t lo = partner<kStep>(static_cast<int>(b)), hi = partner<kStep>(static_cast<int>(b >> 32));
+  return __longlong_as_double(static_cast<int64_t>(uint64_t(hi) << 32 | lo));
+}
+
 // The sum of the values of the row's lanes before this one.
 __device__ __forceinline__ int row_before(int v) {
   int x = v;
@@ -275,21 +295,26 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 // (6.3 + 0.4) 2^-23 (the mean distance to the largest of 512 logits is below their
 // entropy's bound, ln 512) and 36 additions of 2^-24, for which 2^-18 stands.
 //   1. every lane finds the two largest of its C values;
-//   2. groups are ranked by them; two fp32 ranks that are too close decide nothing;
+//   2. groups are ranked by them; where two fp32 ranks are too close to decide, the
+//      values that can be among the two largest are evaluated in 64 bits;
 //   3. the k-th largest T of all lanes' two largest bounds the k-th largest of the
 //      row from below and near: what is below T, less the errors, is out;
 //   4. the rest, a few more than k, go one to a lane (through LDS, in index order),
 //      are ranked by exact 64-bit values by counting, and those below k are chosen.
-// A row that step 2 leaves open, or with more than sixteen values left in step 4
+// A softmax's 64-bit sum is formed only for waves with values that its fp32 one does
+// not tell apart. A row with a NaN, or with more than sixteen values left in step 4
 // (many equal values with a bias), goes to route_exact.
+// Rows read in whole pieces stay in LDS, too, for step 4 (read again from memory they cost 4 us of 36).
 template <int C, bool kBias>
-__global__ __launch_bounds__(kThreads) void route_narrow(RouteArgs p) {
-  extern __shared__ int64_t keys[];         // for route_exact
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(C > 16 ? 2 : kBias ? 3 : 4))) void route_narrow(
+    RouteArgs p) {
+  extern __shared__ int64_t keys[];         // for route_exact, then the rows' logits
   using V = std::conditional_t<kBias, float, int>;
   struct Row {
     union {
       V top[2 * kLanes];
       int64_t key[kLanes];
+      double value[kLanes];
     };
     int id[kLanes];
     float logit[kLanes];
@@ -298,6 +323,7 @@ __global__ __launch_bounds__(kThreads) void route_narrow(RouteArgs p) {
   __shared__ __attribute__((aligned(16))) Row lds[kRows];
   const float err = p.score == MOE_SCORE_SIGMOID ? 0x1p-21f : 0x1p-18f;
   Row& mem = lds[threadIdx.x / kLanes];
+  float* logits = reinterpret_cast<float*>(keys + kWaves * p.E) + threadIdx.x / kLanes * p.E;
   for (int64_t row0 = blockIdx.x * int64_t(kRows); row0 < p.M; row0 += int64_t(gridDim.x) * kRows) {
     // Opaque, or the compiler keeps what depends on it alone in (spilled) scalars across rows.
     const int lane = in_vgpr(threadIdx.x % kLanes);
@@ -331,6 +357,11 @@ __global__ __launch_bounds__(kThreads) void route_narrow(RouteArgs p) {
       for (int i = 0; i < C; ++i)
         l[i] = here && d.first + i < d.end ? load_elem(p.logits, at + d.first + i, p.dtype) : -INFINITY;
     }
+    if (p.vector) {
+#pragma unroll
+      for (int i = 0; i < C / 4; ++i)
+        reinterpret_cast<floatx4*>(logits + d.first)[i] = floatx4{l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]};
+    }
     // The softmax's largest logit and its sum, where something needs them.
     float top = 0.0f, total = 1.0f;
     if (p.score == MOE_SCORE_SOFTMAX && (kBias || !p.renormalize)) {
@@ -344,6 +375,7 @@ __global__ __launch_bounds__(kThreads) void route_narrow(RouteArgs p) {
       total = row_sum(total);
     }
     V v[C];
+    bool open = false;                       // the row goes to route_exact
     if constexpr (kBias) {
       const float inv = __builtin_amdgcn_rcpf(total);
 #pragma unroll
@@ -351,8 +383,8 @@ __global__ __launch_bounds__(kThreads) void route_narrow(RouteArgs p) {
         const float b = d.first + i < d.end ? p.bias[d.first + i] : -INFINITY;
         const float s = p.score == MOE_SCORE_SOFTMAX ? fast_exp(l[i] - top) * inv
                                                      : __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[i]));
-        const float c = s + b;
-        v[i] = l[i] == -INFINITY || b == -INFINITY ? -INFINITY : c != c ? INFINITY : c;
+        v[i] = l[i] == -INFINITY ? -INFINITY : s + b;
+        open |= v[i] != v[i];                // a NaN has no place among fp32 maxima
       }
     } else {
 #pragma unroll
@@ -361,19 +393,35 @@ __global__ __launch_bounds__(kThreads) void route_narrow(RouteArgs p) {
     V a = v[0], b = none<V>();
 #pragma unroll
     for (int i = 1; i < C; ++i) {
-      b = max(b, min(a, v[i]));
+      b = max(min(a, b), min(max(a, b), v[i]));   // the median, one instruction
       a = max(a, v[i]);
     }
-    bool open = false;                       // the row goes to route_exact
+    double total64 = total;                  // the softmax's sum, fp32's until `sum_exactly`
+    const auto logit_at = [&](int e) { return p.vector ? logits[e] : load_elem(p.logits, at + e, p.dtype); };
+    const auto sum_exactly = [&] {
+      double t = 0.0;
+      for (int e = d.first; here && e < d.end; ++e) {
+        const float x = logit_at(e);
+        if (x != -INFINITY) t += exp(static_cast<double>(x) - top);
+      }
+      total64 = row_sum(t);
+    };
+    const auto exact_value = [&](int e, float x) {
+      const double l64 = x;
+      return (p.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-l64)) : exp(l64 - top) / total64) + p.bias[e];
+    };
     if (p.topk_groups < p.groups) {
-      V ga = a, gb = b;
-      const auto merge = [&](V oa, V ob) {
+      const auto merge = [&](auto& ga, auto& gb, auto oa, auto ob) {
         gb = max(min(ga, oa), max(gb, ob));
         ga = max(ga, oa);
       };
-      if (p.narrow.per_group > 1) merge(partner<1>(ga), partner<1>(gb));
-      if (p.narrow.per_group > 2) merge(partner<2>(ga), partner<2>(gb));
-      if (p.narrow.per_group > 4) merge(partner<4>(ga), partner<4>(gb));
+      const auto merge_group = [&](auto& ga, auto& gb) {
+        if (p.narrow.per_group > 1) merge(ga, gb, partner<1>(ga), partner<1>(gb));
+        if (p.narrow.per_group > 2) merge(ga, gb, partner<2>(ga), partner<2>(gb));
+        if (p.narrow.per_group > 4) merge(ga, gb, partner<4>(ga), partner<4>(gb));
+      };
+      V ga = a, gb = b;
+      merge_group(ga, gb);
       V g = ga;
       float close = 0.0f;                    // ranks this near to each other decide nothing
       if constexpr (kBias) {
@@ -385,12 +433,41 @@ __global__ __launch_bounds__(kThreads) void route_narrow(RouteArgs p) {
       mem.top[lane] = g;
       wave_lds_fence();
       int rank = 0;
+      bool unsure = false;
       for (int o = 0; o < p.groups; ++o) {
         const V og = mem.top[o * p.narrow.per_group];
         rank += (og > g || (og == g && o < d.group)) ? 1 : 0;
-        if constexpr (kBias) open |= o != d.group && fabsf(og - g) <= close;
+        if constexpr (kBias) unsure |= o != d.group && g != -INFINITY && fabsf(og - g) <= close;
       }
-      if constexpr (kBias) open = (open || g == INFINITY) && g != -INFINITY;
+      if constexpr (kBias) {
+        unsure |= g == INFINITY;
+        if (__any(unsure)) {
+          if (p.score == MOE_SCORE_SOFTMAX) sum_exactly();
+          const float low = b - (2.0f * err + fabsf(b) * 0x1p-21f);
+          uint32_t near = 0;
+#pragma unroll
+          for (int i = C - 1; i >= 0; --i) near = near + near + (v[i] != -INFINITY && !(v[i] < low) ? 1 : 0);
+          double xa = -INFINITY, xb = -INFINITY;
+          while (near != 0) {
+            const int e = d.first + __ffs(near) - 1;
+            near &= near - 1;
+            const double x = exact_value(e, logit_at(e));
+            xb = max(xb, min(xa, x));
+            xa = max(xa, x);
+          }
+          merge_group(xa, xb);
+          const double x = p.group_top == 2 && xb != -INFINITY ? xa + xb : xa;
+          wave_lds_fence();
+          mem.key[lane] = x == -INFINITY ? kNoKey : key_of(x);
+          wave_lds_fence();
+          const int64_t key = mem.key[lane];
+          rank = 0;
+          for (int o = 0; o < p.groups; ++o) {
+            const int64_t ok = mem.key[o * p.narrow.per_group];
+            rank += (ok > key || (ok == key && o < d.group)) ? 1 : 0;
+          }
+        }
+      }
       if (rank >= p.topk_groups) {
         a = b = none<V>();
 #pragma unroll
@@ -401,26 +478,26 @@ __global__ __launch_bounds__(kThreads) void route_narrow(RouteArgs p) {
     mem.top[lane] = a;
     mem.top[kLanes + lane] = b;
     wave_lds_fence();
-    int na = 0, nb = 0;
+    int from_a = 0, from_b = 0;              // values from a, from b on
 #pragma unroll
     for (int o = 0; o < 2 * kLanes; ++o) {
       const V t = mem.top[o];
-      na += t >= a ? 1 : 0;
-      nb += t >= b ? 1 : 0;
+      from_a += t >= a ? 1 : 0;
+      from_b += t >= b ? 1 : 0;
     }
-    const V bound = row_max(max(na >= p.k ? a : none<V>(), nb >= p.k ? b : none<V>()));
+    const V bound = row_max(max(from_a >= p.k ? a : none<V>(), from_b >= p.k ? b : none<V>()));
     uint32_t left = 0;                       // places that stay
     if constexpr (kBias) {
       const float low = bound == INFINITY ? bound : bound - (2.0f * err + fabsf(bound) * 0x1p-21f);
 #pragma unroll
-      for (int i = 0; i < C; ++i) left |= (v[i] >= low && v[i] != -INFINITY) ? 1u << i : 0u;
+      for (int i = C - 1; i >= 0; --i) left = left + left + (v[i] >= low && v[i] != -INFINITY ? 1 : 0);
     } else {
       // Equal keys are equal values: the first k of those at the bound are enough.
       uint32_t same = 0;
 #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        left |= v[i] > bound ? 1u << i : 0u;
-        same |= v[i] == bound && v[i] != INT32_MIN ? 1u << i : 0u;
+      for (int i = C - 1; i >= 0; --i) {
+        left = left + left + (v[i] > bound ? 1 : 0);
+        same = same + same + (v[i] == bound && v[i] != INT32_MIN ? 1 : 0);
       }
       int room = p.k - row_before(__popc(same));
       for (; room > 0 && same != 0; --room) {
@@ -440,31 +517,37 @@ __global__ __launch_bounds__(kThreads) void route_narrow(RouteArgs p) {
     }
     wave_lds_fence();
     int id = lane < all && !open ? mem.id[lane] : -1;
-    float chosen = id >= 0 ? load_elem(p.logits, at + id, p.dtype) : -INFINITY;
-    int64_t key = kNoKey;
-    if (id >= 0) {
-      double c = chosen;
-      if constexpr (kBias)
-        c = (p.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-c)) : exp(c - top) / total) + p.bias[id];
-      key = key_of(c);
-    }
-    mem.key[lane] = key;
-    wave_lds_fence();
+    float chosen = id < 0 ? -INFINITY : logit_at(id);
     int rank = 0;
-#pragma unroll
-    for (int o = 0; o < kLanes; ++o) {
-      const int64_t t = mem.key[o];
-      rank += (t > key || (t == key && o < lane)) ? 1 : 0;
-      // The softmax's sum is an fp32 one: values as near as its error are not told apart by it.
-      if constexpr (kBias) {
-        if (p.score == MOE_SCORE_SOFTMAX && o != lane && t != kNoKey && key != kNoKey)
-          open |= !(fabs(value_of(t) - value_of(key)) > 2.0 * err);
-      }
-    }
     if constexpr (kBias) {
-      if (p.score == MOE_SCORE_SOFTMAX) open = row_max(open ? 1 : 0) != 0;
+      for (bool exact = p.score == MOE_SCORE_SIGMOID;;) {
+        const double c = id >= 0 ? exact_value(id, chosen) : -INFINITY;
+        mem.value[lane] = c;
+        wave_lds_fence();
+        rank = 0;
+        bool unsure = false;
+#pragma unroll
+        for (int o = 0; o < kLanes; ++o) {
+          const double t = mem.value[o];
+          rank += (t > c || (t == c && o < lane)) ? 1 : 0;
+          unsure |= o != lane && fabs(t - c) <= 2.0 * err;
+        }
+        wave_lds_fence();
+        if (exact || !__any(unsure && id >= 0)) break;
+        sum_exactly();
+        exact = true;
+      }
+    } else {
+      const int key = id >= 0 ? key32(chosen) : INT32_MIN;
+      mem.top[lane] = key;
+      wave_lds_fence();
+#pragma unroll
+      for (int o = 0; o < kLanes; ++o) {
+        const int t = mem.top[o];
+        rank += (t > key || (t == key && o < lane)) ? 1 : 0;
+      }
+      wave_lds_fence();
     }
-    wave_lds_fence();
     if (id >= 0 && rank < p.k) {
       mem.id[rank] = id;
       mem.logit[rank] = chosen;
@@ -646,8 +729,9 @@ RouteLayout layout(int lanes, int groups, int group_size) {
   return y;
 }
 
-// LDS of route_exact's keys for every wave of a workgroup.
+// LDS of route_exact's keys for every wave of a workgroup; of the rows' logits of route_narrow beside them.
 uint32_t exact_bytes(const RouteArgs& p) { return sizeof(int64_t) * kWaves * p.E; }
+uint32_t narrow_bytes(const RouteArgs& p) { return exact_bytes(p) + (p.vector ? sizeof(float) * kRows * p.E : 0); }
 
 template <int C>
 void start_narrow(RouteArgs p, hipStream_t stream) {
@@ -658,9 +742,9 @@ void start_narrow(RouteArgs p, hipStream_t stream) {
              reinterpret_cast<uintptr_t>(p.logits) % 16 == 0;
   const dim3 grid(grid_for((p.M + kRows - 1) / kRows, 0)), block(kThreads);
   if (p.bias != nullptr)
-    launch(route_narrow<C, true>, grid, block, exact_bytes(p), stream, p);
+    launch(route_narrow<C, true>, grid, block, narrow_bytes(p), stream, p);
   else
-    launch(route_narrow<C, false>, grid, block, exact_bytes(p), stream, p);
+    launch(route_narrow<C, false>, grid, block, narrow_bytes(p), stream, p);
 }
 
 }  // namespace

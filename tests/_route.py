@@ -14,7 +14,7 @@ def scores(logits, score):
     if score == SIGMOID:
         return 1.0 / (1.0 + torch.exp(-l))
     top = l.amax(1, keepdim=True)
-    e = torch.exp(l - torch.where(torch.isfinite(top), top, torch.zeros_like(top)))
+    e = torch.exp(l - torch.where(top == -np.inf, torch.zeros_like(top), top))   # an infinite logit: all NaN
     return e / e.sum(1, keepdim=True)
 
 

@@ -161,6 +161,23 @@ def test_nan_and_infinite_logits_show():
         assert ids[0, :2].tolist() == [5, 3] and not bool(w.isnan().any())
 
 
+@pytest.mark.parametrize("E,G,kept", [(64, 8, 3), (256, 8, 4), (512, 16, 5), (96, 32, 9)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_softmax_of_nan_and_infinite_logits_in_groups(E, G, kept, bias):
+    # One such logit makes all scores of its row NaN: groups are equal, the lowest ones kept.
+    g = torch.Generator().manual_seed(6)
+    logits = torch.randn(7, E, generator=g)
+    logits[1, E - 2], logits[2, 3], logits[4, E // 2], logits[4, 1], logits[5, ::2] = float("nan"), INF, INF, float("nan"), -INF
+    b = 0.1 * torch.randn(E, generator=g) if bias else None
+    announce("route nan groups", E, G, bias)
+    for top in (1, 2):
+        kw = dict(groups=G, topk_groups=kept, group_top=top)
+        ids, w = route(logits, 5, b, score=R.SOFTMAX, renormalize=False, **kw)
+        want = R.choose(logits, 5, R.SOFTMAX, b, **kw)
+        assert torch.equal(ids, want), (ids, want)
+        assert bool(w[[1, 2, 4]].isnan().all()) and not bool(w[[0, 3, 5, 6]].isnan().any())
+
+
 GRAD_SHAPES = [(1, 1), (2, 2), (8, 2), (60, 4), (127, 3), (128, 8), (160, 6), (256, 8), (257, 17), (1000, 64),
                (2048, 10)]
 

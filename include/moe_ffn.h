@@ -472,7 +472,7 @@ typedef struct {
  * contributes nothing, whatever its weight.
  *   positions  int32 [M][k] (moe_align_positions), or NULL: route r is row r
  *   topk_w     fp32 [M][k], or NULL: ones (the gradient of a gather of tokens)
- *   y          [M][H] (stride ldy)
+ *   y          [M][H] (stride ldy); may not overlap the inputs
  * Errors of this and the next call: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED
  * (limits above), MOE_ERR_HIP. */
 MOE_API moe_status moe_combine(const moe_combine_desc* d, const void* rows, int64_t ldr, const int32_t* positions,
@@ -505,8 +505,9 @@ typedef struct {
 } moe_matvec_desc;
 
 /* y[t * k + j][n] = sum_i W[topk_ids[t][j]][n][i] x[t][i], W = (q - zero) * scale.
- * Exact products, fp32 sums, rounded once to out_dtype. A row whose ID lies
- * outside [0, E) becomes zero. M == 0 is a no-op.
+ * fp32 sums of exact products (q x and zero x apart, scaled per group), rounded
+ * once to out_dtype; infinities in x make their row's results NaN. A row whose
+ * ID lies outside [0, E) becomes zero. M == 0 is a no-op.
  *   x         [M][K] (stride ldx: a multiple of 8, at most 2^22; 16-byte aligned)
  *   topk_ids  int32 [M][k], or NULL
  *   y         [M * k][N] (stride ldy >= N, at most 2^22); not overlapping inputs

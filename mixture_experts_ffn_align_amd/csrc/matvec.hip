@@ -233,10 +233,14 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void matvec(MatvecArgs p) {
       // Step c: chunk c + 1 (in the order of `turned`) goes to LDS, chunk c + 1 + kAhead is requested, chunk c is multiplied.
       const auto step = [&](int c, int u, bool more) {
         __builtin_amdgcn_sched_barrier(0);   // or later chunks' loads move up and take registers
-        if constexpr (kShare > 1) lds_barrier();
+        if constexpr (kShare > 1)
+          lds_barrier();
+        else
+          asm volatile("" ::: "memory");     // lanes read what others wrote: LDS accesses stay in this order
         if (u % kFlush == 0) {
 #pragma unroll
           for (int f = 0; f < kSteps; ++f) szs[f] = mine.sz[r][f];
+          asm volatile("" ::: "memory");
           const int next = (u / kFlush + 1) % kBatches;
           store_sz(sc[next], ze[next]);
           if (more || u + (1 + kBatches) * kFlush < kUnroll)
@@ -263,6 +267,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void matvec(MatvecArgs p) {
         if (t == kAhead) {
           store_sz(sc0, ze0);
           store(0, w[0], x[0]);
+          asm volatile("" ::: "memory");
         }
         load(c0 + t, w[t % kAhead], x[t % kAhead]);
       }
@@ -330,7 +335,7 @@ void start(MatvecArgs p, int splits, hipStream_t stream) {
 // Few workgroups share the summed index among more waves, many share x among more.
 // Times in us (bf16, groups of 128), N x K, rows, and kShare x splits:
 //   rows <= 4: 512 x 8192, 1 row: 1x8 6.5, 1x4 7.2, 1x2 11.1; 4096 x 2048: 1x4 4.2, 1x8 4.3, 1x2 5.0;
-//     3072 tiles of routed experts, K 2048: 1x2 17.0, 1x4 20.1; 1024 of K 768: 1x2 5.5, 1x4 7.3;
+//     32 routes of 1536 x 2048: 1x2 17.0, 1x4 20.1; 8 of 2048 x 768: 1x2 5.5, 1x4 7.3;
 //     16384 x 8192: chunks of 256, 1x2 18.9, of 128: 1x4 21.0, 1x2 22.3
 //   16 rows: 4096 x 2048: 1x4 5.3, 2x4 6.2, 4x2 7.7; 8192 x 2048: 2x2 6.9, 1x4 7.5, 4x2 8.1;
 //     8192 x 8192: 2x4 14.1, 2x2 15.2, 1x4 15.7; 16384 x 8192: 4x2 21.1, 2x4 29.9, 1x4 33.7

@@ -731,8 +731,8 @@ def _expect_logits(name, t, shape, device=None):
 
 
 def _route_desc(M, E, k, dtype, score, renormalize, scale, groups, topk_groups, group_top):
-    if not 0 <= groups | topk_groups | group_top | score | M | E <= _I32_MAX:
-        _expect_i32(M=M, E=E, score=score, groups=groups, topk_groups=topk_groups, group_top=group_top)
+    if not 0 <= groups | topk_groups | group_top | score | M | E | k <= _I32_MAX:
+        _expect_i32(M=M, E=E, k=k, score=score, groups=groups, topk_groups=topk_groups, group_top=group_top)
     return moe_route_desc(M, E, k, dtype, score, 1 if renormalize else 0, scale, groups, topk_groups, group_top)
 
 
@@ -842,8 +842,8 @@ def moe_combine(rows, positions, topk_w, y, stream=None, check: bool = True) -> 
     M = y.shape[0] if y.dim() == 2 else -1
     ldy = _expect_rows("y", y, (M, H), dev)
     k, pos, w = _slots(positions, topk_w, M, R, dev)
-    if M > _I32_MAX or R > _I32_MAX or H > _I32_MAX:
-        _expect_i32(M=M, rows=R, H=H)
+    if M > _I32_MAX or k > _I32_MAX or R > _I32_MAX or H > _I32_MAX:
+        _expect_i32(M=M, k=k, rows=R, H=H)
     d = moe_combine_desc(M, k, H, R, dt, out)
     st = _call_on(dev, stream, lib().moe_combine, ctypes.byref(d), rows.data_ptr(), ldr, pos, w, y.data_ptr(), ldy)
     if check:
@@ -873,8 +873,8 @@ def moe_combine_grad(dy, rows, positions, topk_w, drows, dtopk_w, stream=None, c
         src = rows.data_ptr()
         _expect_like("dtopk_w", dtopk_w, torch.float32, (M, k), dev)
         dw = dtopk_w.data_ptr()
-    if M > _I32_MAX or R > _I32_MAX or H > _I32_MAX:
-        _expect_i32(M=M, rows=R, H=H)
+    if M > _I32_MAX or k > _I32_MAX or R > _I32_MAX or H > _I32_MAX:
+        _expect_i32(M=M, k=k, rows=R, H=H)
     d = moe_combine_desc(M, k, H, R, dt, ydt)
     st = _call_on(dev, stream, lib().moe_combine_grad, ctypes.byref(d), dy.data_ptr(), lddy, src, ldr, pos, w,
                   drows.data_ptr(), lddr, dw)
@@ -919,8 +919,8 @@ def moe_matvec_int4(x, w, y, topk_ids=None, stream=None, check: bool = True) -> 
         _expect_like("topk_ids", topk_ids, torch.int32, (M, k), dev)
         ids, ldy = topk_ids.data_ptr(), N
         _expect_like("y", y, y.dtype, (M, k, N), dev)
-    if M > _I32_MAX or K > _I32_MAX or N > _I32_MAX or E > _I32_MAX or group > _I32_MAX:
-        _expect_i32(M=M, K=K, N=N, E=E, group=group)
+    if M > _I32_MAX or k > _I32_MAX or K > _I32_MAX or N > _I32_MAX or E > _I32_MAX or group > _I32_MAX:
+        _expect_i32(M=M, k=k, K=K, N=N, E=E, group=group)
     d = moe_matvec_desc(M, k, E, N, K, dt, out, moe_weights(w.fmt, group, q.data_ptr(), scale.data_ptr(), z))
     st = _call_on(dev, stream, lib().moe_matvec_int4, ctypes.byref(d), x.data_ptr(), ldx, ids, y.data_ptr(), ldy)
     if check:

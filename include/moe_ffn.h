@@ -448,8 +448,9 @@ MOE_API moe_status moe_route_grad(const moe_route_desc* d, const void* logits, i
 /* The inverse of an alignment: positions[r] = the aligned row that holds route
  * r, -1 for a route without one; int32 [routes], from moe_align's
  * sorted_route_ids (capacity entries, of which those below num_padded count;
- * entries outside [0, routes) are padding) in any order. A route named twice gets
- * one of its rows.
+ * entries outside [0, routes) are padding) in any order. Each route must appear at
+ * most once, as in every alignment (of several rows a route gets one, and which one
+ * may differ from call to call).
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (more than 2^31 - 256 routes
  * or rows), MOE_ERR_HIP. */
 MOE_API moe_status moe_align_positions(const int32_t* sorted_route_ids, const int32_t* num_padded, size_t capacity,

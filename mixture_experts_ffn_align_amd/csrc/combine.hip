@@ -179,7 +179,10 @@ __global__ __launch_bounds__(kThreads) void combine_grad(CombineArgs p) {
 }
 
 // positions[r] = the row of route r, -1 without one. The fill comes before the
-// scatter: by a barrier in one workgroup, by a second launch in several.
+// scatter: by a barrier in one workgroup, by a second launch in several. Routes
+// have one row each, so the stores meet no others (a maximum by atomics, which
+// would order them, takes 6.5 us for 4096 routes in place of 3.4, 43 for 2^20 in
+// place of 16).
 __device__ __forceinline__ void scatter_positions(const int32_t* sorted, int live, int routes, int32_t* positions,
                                                   int first, int step) {
   constexpr int kBatch = 4;                 // loads in flight

@@ -18,6 +18,7 @@
 // wave's share of the summed index.
 #include "common.hpp"
 #include "kernels.hpp"
+#include "matvec_shape.hpp"
 
 namespace moe {
 
@@ -313,67 +314,50 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void matvec(MatvecArgs p) {
 }
 
 template <bool kHalf, int kChunk, int kRows, int kShare>
-void start(MatvecArgs p, int splits, hipStream_t stream) {
+void start(MatvecArgs p, const MatvecShape& c, hipStream_t stream) {
   const int64_t tiles = (p.N + kTile * kShare - 1) / (kTile * kShare);
   const int64_t blocks = p.ids != nullptr ? p.rows : (p.rows + kRows - 1) / kRows;
   p.tasks = tiles * blocks;
   // Products of 32 elements to their group: exact for the 2^15 + 2^7 that are asked for at most.
   p.group_inverse = static_cast<uint32_t>(((uint64_t(1) << 31) + p.group / 32 - 1) / (p.group / 32));
-  const int waves = splits * kShare;
+  const int waves = c.splits * kShare;
   const dim3 grid(grid_for(p.tasks, 0)), block(waves * kWave);
-  uint32_t lds = waves * (2 * kTile * kChunk / 2 + kTile * kChunk / 8) + splits * 2 * kRows * kChunk * 2;
-  const uint32_t sums = (splits - 1) * kShare * ((kRows + kTile - 1) / kTile) * kWave * 16;
+  uint32_t lds = waves * (2 * kTile * kChunk / 2 + kTile * kChunk / 8) + c.splits * 2 * kRows * kChunk * 2;
+  const uint32_t sums = (c.splits - 1) * kShare * ((kRows + kTile - 1) / kTile) * kWave * 16;
   lds = lds > sums ? lds : sums;
-  if (p.group % 128 == 0)
+  if (c.flush == 4)
     launch(matvec<kHalf, kChunk, kRows, kShare, 4>, grid, block, lds, stream, p);
-  else if (p.group % 64 == 0)
+  else if (c.flush == 2)
     launch(matvec<kHalf, kChunk, kRows, kShare, 2>, grid, block, lds, stream, p);
   else
     launch(matvec<kHalf, kChunk, kRows, kShare, 1>, grid, block, lds, stream, p);
 }
 
-// Few workgroups share the summed index among more waves, many share x among more.
-// Times in us (bf16, groups of 128), N x K, rows, and kShare x splits:
-//   rows <= 4: 512 x 8192, 1 row: 1x8 6.5, 1x4 7.2, 1x2 11.1; 4096 x 2048: 1x4 4.2, 1x8 4.3, 1x2 5.0;
-//     32 routes of 1536 x 2048: 1x2 17.0, 1x4 20.1; 8 of 2048 x 768: 1x2 5.5, 1x4 7.3;
-//     16384 x 8192: chunks of 256, 1x2 18.9, of 128: 1x4 21.0, 1x2 22.3
-//   16 rows: 4096 x 2048: 1x4 5.3, 2x4 6.2, 4x2 7.7; 8192 x 2048: 2x2 6.9, 1x4 7.5, 4x2 8.1;
-//     8192 x 8192: 2x4 14.1, 2x2 15.2, 1x4 15.7; 16384 x 8192: 4x2 21.1, 2x4 29.9, 1x4 33.7
-//   64 rows: 512 x 8192: 2x4 30, 2x2 34, 4x2 43; 8192 x 2048: 2x2 15.5, 2x4 18.1, 4x2 20.8;
-//     16384 x 8192: 4x2 54.5, 4x1 59.9, 2x2 61.5; 200 rows, 8192 x 2048: 4x1 28.7, 2x2 39.3, 4x2 41.7;
-//     37 rows, 5001 x 4064, groups of 32: 2x4 16.7, 2x2 18.2, 4x2 24.3
 template <bool kHalf, int kRows>
-void by_tiles(const MatvecArgs& p, int64_t tiles, hipStream_t stream) {
-  if (tiles < 1024)
-    start<kHalf, 128, kRows, 2>(p, p.K > 2048 ? 4 : 2, stream);
+void by_share(const MatvecArgs& p, const MatvecShape& c, hipStream_t stream) {
+  if (c.share == 2)
+    start<kHalf, 128, kRows, 2>(p, c, stream);
   else
-    start<kHalf, 128, kRows, 4>(p, tiles < 2048 ? 2 : 1, stream);
+    start<kHalf, 128, kRows, 4>(p, c, stream);
 }
 
 template <bool kHalf>
 void by_shape(const MatvecArgs& p, hipStream_t stream) {
-  const int64_t rows = p.ids != nullptr ? 1 : p.rows;
-  const int64_t tiles = (p.N + kTile - 1) / kTile * (p.ids != nullptr ? p.rows : (p.rows + 4 * kTile - 1) / (4 * kTile));
-  if (rows <= 4) {
-    if (tiles >= 1024 && p.K >= 4096)
-      start<kHalf, 256, 4, 1>(p, 2, stream);
-    else
-      start<kHalf, 128, 4, 1>(p, tiles > 1024 || (tiles >= 1024 && p.K < 1024) ? 2 : tiles <= 256 && p.K >= 4096 ? 8 : 4,
-                              stream);
-  } else if (rows <= kTile) {
-    if (tiles < 512)
-      start<kHalf, 128, 16, 1>(p, 4, stream);
-    else if (tiles < 1024)
-      start<kHalf, 128, 16, 2>(p, p.K >= 8192 ? 4 : 2, stream);
-    else
-      start<kHalf, 128, 16, 4>(p, 2, stream);
-  } else if (rows <= 2 * kTile) {
-    by_tiles<kHalf, 32>(p, tiles, stream);
-  } else if (rows <= 3 * kTile) {
-    by_tiles<kHalf, 48>(p, tiles, stream);
-  } else {
-    by_tiles<kHalf, 64>(p, tiles, stream);
-  }
+  const MatvecShape c = matvec_shape(p.ids != nullptr, p.rows, p.N, p.K, p.group);
+  if (c.chunk == 256)
+    start<kHalf, 256, 4, 1>(p, c, stream);
+  else if (c.rows == 4)
+    start<kHalf, 128, 4, 1>(p, c, stream);
+  else if (c.rows == 16 && c.share == 1)
+    start<kHalf, 128, 16, 1>(p, c, stream);
+  else if (c.rows == 16)
+    by_share<kHalf, 16>(p, c, stream);
+  else if (c.rows == 32)
+    by_share<kHalf, 32>(p, c, stream);
+  else if (c.rows == 48)
+    by_share<kHalf, 48>(p, c, stream);
+  else
+    by_share<kHalf, 64>(p, c, stream);
 }
 
 }  // namespace

@@ -36,6 +36,18 @@ def test_rule_gives_built_shapes_only(shape):
                     assert routed or c[1] >= min(rows, 64)
 
 
+def test_no_rule_for_one_count_of_tiles(shape):
+    # Where the summed index changes the count of tiles from which another shape is taken, it does so by a range
+    # of counts, not by one.
+    for rows in (1, 16, 64):
+        edges = set()
+        for K in (256, 768, 1024, 1536, 2048, 4064):
+            shapes = [shape(False, rows, 16 * tiles, K, 32) for tiles in range(500, 2100)]
+            edges |= {500 + i for i in range(1, len(shapes)) if shapes[i] != shapes[i - 1]}
+        edges = sorted(edges)
+        assert all(b - a >= 64 for a, b in zip(edges, edges[1:])), (rows, edges)
+
+
 def exact(x, q, s, z, group):
     """fp64 [M, N] on the GPU: whole numbers times quarters, so sums are exact in any order."""
     v = torch.empty(*q.shape, 8, dtype=torch.float64, device="cuda")

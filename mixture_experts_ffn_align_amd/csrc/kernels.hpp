@@ -36,7 +36,9 @@ void launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, uint32_t lds_bytes,
 // Every kernel strides over its tasks, so its grid may be smaller than its
 // task count; launches are capped at kMaxGrid workgroups (and at a caller's
 // max_workgroups > 0), which keeps the work-item count of a dispatch within
-// 32 bits. Task counts themselves are int32 (the C ABI rejects larger layers).
+// 32 bits. Task counts themselves are int32 in the layer and the ragged products
+// (the C ABI rejects larger ones) and 64 bits wide in routing, the sums of routes
+// and the 4-bit products, whose limits on sizes admit more.
 constexpr int64_t kMaxGrid = int64_t(1) << 20;
 inline int grid_for(int64_t work_groups, int max_workgroups) {
   if (work_groups < 1) work_groups = 1;

@@ -301,14 +301,20 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 //   2. groups are ranked by them; where two fp32 ranks are too close to decide, the
 //      values that can be among the two largest are evaluated in 64 bits;
 //   3. the k-th largest T of all lanes' two largest bounds the k-th largest of the
-//      row from below and near: what is below T, less the errors, is out;
+//      row from below: what is below T, less the errors, is out. That is near where k
+//      is well below the number of those values (256 experts, 13 slots: 4 % of the rows
+//      keep more than sixteen) and not where many slots or few groups make k of them
+//      most (16 slots: 80 %; 6 slots of one of eight groups: all). Such a row bisects
+//      its ordered keys for a T that at least k and at most sixteen values reach;
 //   4. the rest, a few more than k, go one to a lane (through LDS, in index order),
 //      are ranked by exact 64-bit values by counting, and those below k are chosen.
 // A softmax's 64-bit sum is formed only for waves with values that its fp32 one does
 // not tell apart. A row with a NaN, or with more than sixteen values left in step 4
-// (many equal values with a bias), goes to route_exact. Bound: VALU and its waits
-// (1250 instructions a wave, three waves a SIMD): 32768 rows of 256 experts in
-// groups, with a bias, 29 us; without bias and groups 15.
+// (with a bias: values equal to the k-th within the errors), goes to route_exact.
+// Bound: VALU and its waits (1250 instructions a wave, three waves a SIMD): 32768
+// rows of 256 experts in groups, with a bias, 8 slots 31 us, 12 slots 34, 16 slots 55
+// (before the bisection 31, 100, 231; a wave a row 84, 107, 128); eight slots of one
+// group 41 (157; 84); without bias and groups 8 slots 16, 16 slots 24 (16, 161; 120).
 // Rows read in whole pieces stay in LDS, too, for step 4 (read again from memory they cost 4 us of 36).
 template <int C, bool kBias>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(C > 16 ? 2 : kBias ? 3 : 4))) void route_narrow(
@@ -506,29 +512,66 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(C > 16
       from_a += t >= a ? 1 : 0;
       from_b += t >= b ? 1 : 0;
     }
-    const V bound = row_max(max(from_a >= p.k ? a : none<V>(), from_b >= p.k ? b : none<V>()));
-    uint32_t left = 0;                       // places that stay
-    if constexpr (kBias) {
-      const float low = bound == INFINITY ? bound : bound - (2.0f * err + fabsf(bound) * 0x1p-21f);
+    V bound = row_max(max(from_a >= p.k ? a : none<V>(), from_b >= p.k ? b : none<V>()));
+    uint32_t left;                           // places that stay
+    const auto keep = [&](int larger) {      // at least so many values above the bound
+      left = 0;
+      if constexpr (kBias) {
+        const float low = bound == INFINITY ? bound : bound - (2.0f * err + fabsf(bound) * 0x1p-21f);
 #pragma unroll
-      for (int i = C - 1; i >= 0; --i) left = left + left + (v[i] >= low && v[i] != -INFINITY ? 1 : 0);
-    } else {
-      // Equal keys are equal values: the first k of those at the bound are enough.
-      uint32_t same = 0;
+        for (int i = C - 1; i >= 0; --i) left = left + left + (v[i] >= low && v[i] != -INFINITY ? 1 : 0);
+      } else {
+        // Equal keys are equal values: the first of those at the bound are enough.
+        uint32_t same = 0;
 #pragma unroll
-      for (int i = C - 1; i >= 0; --i) {
-        left = left + left + (v[i] > bound ? 1 : 0);
-        same = same + same + (v[i] == bound && v[i] != INT32_MIN ? 1 : 0);
+        for (int i = C - 1; i >= 0; --i) {
+          left = left + left + (v[i] > bound ? 1 : 0);
+          same = same + same + (v[i] == bound && v[i] != INT32_MIN ? 1 : 0);
+        }
+        int room = p.k - larger - row_before(__popc(same));
+        for (; room > 0 && same != 0; --room) {
+          left |= same & -same;
+          same &= same - 1;
+        }
       }
-      int room = p.k - row_before(__popc(same));
-      for (; room > 0 && same != 0; --room) {
-        left |= same & -same;
-        same &= same - 1;
+      return row_sum(static_cast<int>(__popc(left)));
+    };
+    int all = keep(0);
+    if (__any(all > kLanes)) {
+      // Many slots on few lanes. Where no value has at most sixteen at or above it, the k-th largest itself is found.
+      const auto key = [](V t) { if constexpr (kBias) return key32(t); else return t; };
+      const auto value = [](int t) { if constexpr (kBias) return logit_of(t); else return t; };
+      int lo = key(bound), hi = key(row_max(a));      // k values at least reach lo
+      if (lo == INT32_MIN) {
+        int least = INT32_MAX;
+#pragma unroll
+        for (int i = 0; i < C; ++i) least = min(least, v[i] == none<V>() ? INT32_MAX : key(v[i]));
+        lo = -row_max(-least);
       }
+      bool going = all > kLanes && lo < hi;
+      while (__any(going)) {
+        const int mid = lo + static_cast<int>((static_cast<uint32_t>(hi) - static_cast<uint32_t>(lo) + 1) / 2);
+        const V t = value(mid);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < C; ++i) n += v[i] >= t ? 1 : 0;
+        n = row_sum(n);
+        if (going && n >= p.k) lo = mid;
+        if (going && n < p.k) hi = mid - 1;
+        going = going && lo < hi && !(n >= p.k && n <= kLanes);
+      }
+      int larger = 0;
+      if constexpr (!kBias) {
+        if (all > kLanes) bound = lo;
+#pragma unroll
+        for (int i = 0; i < C; ++i) larger += v[i] > bound ? 1 : 0;
+        larger = row_sum(larger);
+      } else if (all > kLanes) {
+        bound = value(lo);
+      }
+      all = keep(larger);
     }
-    const int count = __popc(left);
-    int slot = row_before(count);
-    const int all = row_sum(count);
+    int slot = row_before(__popc(left));
     open = row_max(open || all > kLanes ? 1 : 0) != 0;
     if (!open) {
       while (left != 0) {
@@ -770,8 +813,10 @@ void start_narrow(RouteArgs p, hipStream_t stream) {
 
 }  // namespace
 
-// Sixteen lanes a row where they hold it (32768 tokens, 256 experts in groups with a bias: 29 us, a wave a row 115;
-// 4096 tokens, 128 experts: 5.6 and 12.4; one token 4.6 and 7.7), a wave for more experts, slots or groups.
+// Sixteen lanes a row where they hold it (32768 tokens, 256 experts, eight groups with a bias, four kept: 1, 8 and 16
+// slots 30, 31 and 55 us, a wave a row 47, 84 and 128; one kept, 4, 8 and 16 slots: 30, 41, 59 and 63, 84, 125; 512
+// experts, 8 slots: 52 and 102; 2048 tokens, 256 experts, 8 and 14 slots: 7.9, 9.6 and 12.1, 17.3, but 1 and 16, of which
+// some row has a seventeenth within the errors: 7.8, 24.7 and 6.6, 18.9), a wave for more experts, slots or groups.
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
   RouteArgs p = a;
   p.group_size = p.E / p.groups;

@@ -421,8 +421,11 @@ typedef struct {
  *   bias      fp32 [E] or NULL
  *   topk_ids  int32 [M][k] out;  topk_w fp32 [M][k] out
  * The choice is exact: it is made on the logits, or on scores evaluated in 64
- * bits, not on fp32 scores whose rounding would order close experts. Weights
- * are fp32.
+ * bits, not on fp32 scores whose rounding would order close experts (those closer
+ * than a few last places of 64 bits have that arithmetic's order). Weights are
+ * fp32. In the softmax's sum for weights that are not renormalised, and in all of
+ * their gradient, an exponential whose logit is x below the row's largest is within
+ * |x| 2^-23 + 2^-22 of its value, relatively.
  * An expert whose logit or bias is -infinity is never chosen and has no part in
  * its group's rank; where fewer than k are left, the rest of the row is expert
  * -1 (an invalid route) with weight 0. A NaN choice value ranks above every
@@ -507,8 +510,11 @@ typedef struct {
 
 /* y[t * k + j][n] = sum_i W[topk_ids[t][j]][n][i] x[t][i], W = (q - zero) * scale.
  * fp32 sums of exact products (q x and zero x apart, scaled per group), rounded
- * once to out_dtype; infinities in x make their row's results NaN. A row whose
- * ID lies outside [0, E) becomes zero. M == 0 is a no-op.
+ * once to out_dtype; infinities in x make their row's results NaN, and so may bf16
+ * values of 2^116 and above, which overflow those sums. The order of a row's sums
+ * depends on N, K and the number of rows: its last bits may differ between batches
+ * of other sizes. A row whose ID lies outside [0, E) becomes zero. M == 0 is a
+ * no-op.
  *   x         [M][K] (stride ldx: a multiple of 8, at most 2^22; 16-byte aligned)
  *   topk_ids  int32 [M][k], or NULL
  *   y         [M * k][N] (stride ldy >= N, at most 2^22); not overlapping inputs

@@ -287,7 +287,9 @@ __device__ __forceinline__ int row_before(int v) {
 // The logit of a key32 that is none of its ends.
 __device__ __forceinline__ float logit_of(int key) { return __int_as_float(key ^ ((key >> 31) & INT32_MAX)); }
 
-// e^x from the hardware's 2^x: within |x| 2^-23 + 2^-22 of it, relatively.
+// e^x from the hardware's 2^x: within |x| 2^-23 + 2^-22 of it, relatively. It serves the choice, whose bounds
+// count it, and the sum and the gradient over a whole row, where it weighs p |x| 2^-23: below 2^-24 of the largest score.
+// A chosen expert's weight takes expf.
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
 // Sixteen lanes take a row, so a wave chooses for four at once. Values to rank

@@ -88,3 +88,56 @@ def test_exact_in_every_shape(case, dtype, shape):
     rows = torch.arange(M, device="cuda").unsqueeze(-1)
     want = torch.where(here, all_of[ids.clamp(0, E - 1).long(), rows], torch.zeros((), dtype=torch.float64, device="cuda"))
     assert torch.equal(y.double(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=str)
+@pytest.mark.parametrize("N,K,group", [(72, 1056, 32), (8197, 2176, 128)])
+def test_rows_in_batches_of_other_sizes(N, K, group, dtype, shape):
+    # By the same kernel a row has the same bits whatever stands beside it; by another its sums have another order,
+    # and both are within the bound of fp32 sums.
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dev = dict(generator=g, device="cuda")
+    q = torch.randint(-2 ** 31, 2 ** 31, (1, N, K // 8), dtype=torch.int32, **dev)
+    s = (0.002 + 0.008 * torch.rand(1, N, K // group, **dev)).half()
+    z = torch.randint(0, 16, s.shape, dtype=torch.uint8, **dev)
+    p = moe.DeviceProjection(moe.MOE_W_INT4_AWQ, group, q, s, z)
+    x = torch.randn(64, K, **dev).to(dtype)
+    print("[gpu-case] matvec batches", N, K, dtype, flush=True)
+    whole = torch.empty(64, N, device="cuda")
+    moe.moe_matvec_int4(x, p, whole)
+    ref = exact(x, q[0], s[0], z[0], group)
+    # A group sums (16 + q) x and x, each addition off by a step of a partial sum; the groups' sums, scaled, add up
+    # over K / group steps, and seven between waves.
+    scale = s[0].double().repeat_interleave(group, -1)
+    zero = z[0].double().repeat_interleave(group, -1)
+    bound = (2 * group + 4 + K / group + 7) * 2.0 ** -23 * (x.double().abs() @ (scale * (32.0 + zero)).T)
+    same = 0
+    for a, b in ((0, 64), (0, 49), (7, 64), (3, 60), (0, 48), (16, 64), (0, 16), (5, 6), (40, 64), (60, 64)):
+        y = torch.empty(b - a, N, device="cuda")
+        moe.moe_matvec_int4(x[a:b], p, y)
+        if shape(False, b - a, N, K, group) == shape(False, 64, N, K, group):
+            assert torch.equal(y, whole[a:b])
+            same += 1
+        assert bool(((y.double() - ref[a:b]).abs() <= bound[a:b]).all())
+    assert same == 4
+
+
+@pytest.mark.gpu
+def test_largest_inputs_that_do_not_overflow():
+    # A sum of 128 products is below 128 * 31 |x| < 2^12 |x|: bf16 inputs below 2^116 stay within fp32.
+    N, K = 40, 512
+    g = torch.Generator(device="cuda").manual_seed(6)
+    dev = dict(generator=g, device="cuda")
+    print("[gpu-case] matvec largest inputs", flush=True)
+    for group in (32, 64, 128, 512):
+        q = torch.randint(-2 ** 31, 2 ** 31, (1, N, K // 8), dtype=torch.int32, **dev)
+        q[:, 0], q[:, 1] = -1, 0                                   # the largest and the smallest sums
+        s = torch.full((1, N, K // group), 2.0 ** -14, dtype=F16, device="cuda")
+        z = torch.randint(0, 16, s.shape, dtype=torch.uint8, **dev)
+        z[:, 0], z[:, 1] = 0, 15
+        x = torch.where(torch.rand(5, K, **dev) < 0.5, -(2.0 ** 115), 2.0 ** 115)
+        x[0] = 2.0 ** 115
+        y = torch.empty(5, N, device="cuda")
+        moe.moe_matvec_int4(x.to(BF16), moe.DeviceProjection(moe.MOE_W_INT4_AWQ, group, q, s, z), y)
+        assert torch.equal(y.double(), exact(x, q[0], s[0], z[0], group))     # whole numbers of 2^101, below 2^13 of them

@@ -543,6 +543,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(C > 16
       // Many slots on few lanes. Where no value has at most sixteen at or above it, the k-th largest itself is found.
       const auto key = [](V t) { if constexpr (kBias) return key32(t); else return t; };
       const auto value = [](int t) { if constexpr (kBias) return logit_of(t); else return t; };
+      // Opaque, or comparisons are kept from `keep` above, as scalars that others are spilled for.
+#pragma unroll
+      for (int i = 0; i < C; ++i) asm volatile("" : "+v"(v[i]));
       int lo = key(bound), hi = key(row_max(a));      // k values at least reach lo
       if (lo == INT32_MIN) {
         int least = INT32_MAX;
